@@ -528,6 +528,158 @@ lora_status_t lora_linear_ce_fwd_bwd(const lora_ce_desc* desc, const void* H, co
                                      const float* dloss, float* loss, float* lse, void* dH, void* workspace,
                                      size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The rest of an attention block around the LoRA linears: layer norm for
+ * models that use it in place of RMSNorm, rotary positions in layouts that the
+ * projection's epilogue does not cover, and the attention itself over packed
+ * documents.  Each stands beside an operator above and follows the conventions
+ * at the top of this file.
+ * ------------------------------------------------------------------------ */
+
+/* Layer norm, per token (row of d features):
+ *   mean = sum(x) / d, rstd = 1 / sqrt(sum((x - mean)^2) / d + eps),
+ *   Y = bf16((x - mean) * rstd * g + b).
+ * X [M x d] bf16, g [d] bf16, b [d] bf16 or NULL (no shift); Y [M x d] bf16,
+ * mean [M] and rstd [M] fp32 (written; the backward's inputs).  Sums in fp32.
+ * Y may be X.  8 <= d <= 16384 (LORA_ERR_UNSUPPORTED above), d % 8 == 0 and X, g, b, Y 16-byte, mean
+ * and rstd 4-byte aligned (LORA_ERR_ALIGNMENT); eps >= 0 and finite, M >= 0
+ * (LORA_ERR_INVALID_ARG).  M == 0 launches nothing. */
+lora_status_t lora_linear_layernorm_fwd(const void* X, const void* g, const void* b, int64_t M, int64_t d, float eps,
+                                        void* Y, float* mean, float* rstd, void* stream);
+
+/* Workspace bytes of lora_linear_layernorm_bwd; 0 for sizes it does not serve. */
+size_t lora_linear_layernorm_workspace_size(int64_t M, int64_t d);
+
+/* Backward of the layer norm:
+ *   dh = dY * g, x_hat = (x - mean) * rstd,
+ *   dX = bf16(rstd * (dh - mean(dh) - x_hat * mean(dh * x_hat))),
+ *   dg = sum over tokens of dY * x_hat, db = sum over tokens of dY.
+ * dY [M x d]: bf16 (dy_f32 == 0; e.g. a projection's dX), or fp32 (dy_f32 == 1;
+ * the sum that lora_linear_bwd_rope leaves).  dX [M x d] bf16; dg, db [d] fp32
+ * (written, 4-byte aligned; each may be NULL).  dX may be dY when dY is bf16, or X.  dg and db are summed in
+ * fp32 in an order fixed by M, d and the device: the same bits in every call.
+ * M == 0 zero-fills dg and db.  Other checks as the forward;
+ * workspace >= lora_linear_layernorm_workspace_size(M, d) bytes. */
+lora_status_t lora_linear_layernorm_bwd(const void* dY, int dy_f32, const void* X, const void* g, const float* mean,
+                                        const float* rstd, int64_t M, int64_t d, void* dX, float* dg, float* db,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Scalings of rotary tables for contexts longer than the one a model was
+ * trained on (`original` positions).  f_i = base^(-2 i / rot) is pair i's
+ * angle per position. */
+typedef enum lora_rotary_scaling_t {
+    LORA_ROTARY_PLAIN = 0,       /* f_i */
+    LORA_ROTARY_LINEAR = 1,      /* f_i / factor */
+    LORA_ROTARY_NTK = 2,         /* base * factor^(rot / (rot - 2)) in place of base */
+    LORA_ROTARY_WAVELENGTH = 3,  /* f_i k + f_i / factor (1 - k), k = the turns that pair i makes over `original`
+                                    positions, from `low` (k = 0) to `high` (k = 1) turns, clamped */
+    LORA_ROTARY_RAMP = 4         /* the same blend with k falling from 1 to 0 along the pair index, from
+                                    floor(at(high)) to ceil(at(low)) (not outside 0 .. rot - 1), at(n) = the index
+                                    whose pair makes n turns: rot ln(original / (2 pi n)) / (2 ln base) */
+} lora_rotary_scaling_t;
+
+typedef struct lora_rotary_table_desc {
+    int64_t n_pos;       /* rows */
+    int32_t rot;         /* rotated features of a head: a multiple of 16 up to 256 */
+    int32_t scaling;     /* lora_rotary_scaling_t */
+    double base;         /* > 1 */
+    double factor;       /* >= 1 (not read by PLAIN) */
+    double low, high;    /* WAVELENGTH, RAMP: 0 < low < high */
+    double original;     /* WAVELENGTH, RAMP: > 0 */
+    double amplitude;    /* multiplies both tables (1: none); > 0 */
+} lora_rotary_table_desc;
+
+/* cos, sin: device fp32 [n_pos x rot/2], written, 16-byte aligned: the tables
+ * of lora_rope_desc and lora_linear_rotary.  Angles are reduced in 64 bits.
+ * LORA_ERR_INVALID_ARG for a field outside the ranges above,
+ * LORA_ERR_UNSUPPORTED for rot.  n_pos == 0 launches nothing. */
+lora_status_t lora_linear_rotary_tables(const lora_rotary_table_desc* desc, float* cos, float* sin, void* stream);
+
+typedef struct lora_rotary_desc {
+    int64_t M;             /* tokens */
+    int32_t heads;         /* of Q (>= 1) */
+    int32_t kv_heads;      /* of K (0: no K) */
+    int32_t head_dim;      /* a multiple of 8 up to 256 */
+    int32_t rot;           /* the first rot features of a head are turned: a multiple of 16, 16 .. head_dim */
+    int32_t interleaved;   /* 0: pairs (i, i + rot/2); 1: pairs (2 i, 2 i + 1) */
+    int32_t inverse;       /* 1: the adjoint, i.e. the opposite angle (the backward pass on dQ, dK) */
+} lora_rotary_desc;
+
+/* Turns finished q and k: Yq, Yk [M x heads * head_dim] bf16 from Q, K, in one
+ * launch, by the table rows at each token's position (pos, cos, sin and n_pos of
+ * `rope`; its head_dim is not read, its tables have rot / 2 columns).  The
+ * features past rot are copied.  Yq may be Q and Yk may be K (both or neither:
+ * LORA_ERR_INVALID_ARG).  A position outside the tables sets status bit 0x2 and
+ * leaves that token unturned.  For q and k that come straight from a
+ * LoRA projection in the half layout with whole heads of 64 or 128,
+ * lora_linear_fwd_rope turns them before they are rounded.
+ * 16-byte aligned tensors, 4-byte aligned pos; workspace >= 256 bytes. */
+lora_status_t lora_linear_rotary(const lora_rotary_desc* desc, const lora_rope_desc* rope, const void* Q,
+                                 const void* K, void* Yq, void* Yk, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* Attention over packed documents.
+ *   z_ij = scale q_i.k_j, or cap tanh(scale q_i.k_j / cap) with softcap = cap > 0,
+ *          minus slopes[h] |i - j| with slopes;
+ *   O_i = sum_j p_ij v_j, p_ij = exp(z_ij - lse_i), lse_i = log sum_j exp(z_ij)
+ * over the keys j that row i sees: those of its own document, with causal != 0
+ * only j <= i or j among the first prefix_len rows of the document.  Query head
+ * h reads key / value head h / (heads / kv_heads). */
+typedef struct lora_attn_desc {
+    int64_t M;           /* rows of the batch, 0 .. 2^30 */
+    int64_t n_docs;      /* documents, >= 0 */
+    int32_t heads;       /* query heads: a multiple of kv_heads, up to 4096 */
+    int32_t kv_heads;
+    int32_t head_dim;    /* 64 or 128 (LORA_ERR_UNSUPPORTED otherwise) */
+    int32_t causal;      /* 0: every row sees its whole document */
+    float scale;         /* > 0, finite */
+    float softcap;       /* 0: none; else > 0, finite */
+} lora_attn_desc;
+
+/* The plan of a batch: its documents as lists of tiles.  It depends on the
+ * documents alone, so all layers (and the backward) of a step share one.
+ * starts: device int32 [n_docs + 1], the documents' first rows: starts[0] = 0,
+ *   not falling, starts[n_docs] <= M.  Documents may be empty.  Rows from
+ *   starts[n_docs] on are behind the last document: their O and gradients are
+ *   zero and their lse is -inf, whatever the inputs hold there.
+ * prefix_len: device int32 [n_docs], 0 .. the document's length, or NULL (0).
+ *   Not read when causal == 0.
+ * plan: device, >= lora_linear_attn_plan_size(M, n_docs) bytes, 16-byte
+ *   aligned; its first word is a status word (lora_linear_device_status), which
+ *   this call sets to 0, or to 0x2 for starts or prefix_len outside the ranges
+ *   above: attention on such a plan computes nothing.  The plan does not
+ *   refer to starts and prefix_len afterwards.  Calls that only read a plan
+ *   (forward, backward) may overlap in time.
+ * lora_linear_attn_plan_size returns 0 for sizes it does not serve. */
+size_t lora_linear_attn_plan_size(int64_t M, int64_t n_docs);
+lora_status_t lora_linear_attn_plan(const int32_t* starts, const int32_t* prefix_len, int64_t M, int64_t n_docs,
+                                    int causal, void* plan, size_t plan_bytes, void* stream);
+
+/* Forward.  Q, O [M x heads * head_dim] bf16, K, V [M x kv_heads * head_dim]
+ * bf16, lse [M x heads] fp32 (written; natural logarithm); slopes: device fp32
+ * [heads] or NULL.  plan: of this M, n_docs and causal; a plan of other sizes
+ * sets its status bit 0x2 and nothing is computed.  A document whose rows hold
+ * infinities or NaN leaves the other documents' results as they are.  No
+ * workspace.  p is rounded to bf16 for the product with v; scores, sums and
+ * outputs are accumulated in fp32. */
+lora_status_t lora_linear_attn_fwd(const lora_attn_desc* desc, void* plan, size_t plan_bytes, const void* Q,
+                                   const void* K, const void* V, const float* slopes, void* O, float* lse,
+                                   void* stream);
+
+/* Workspace bytes of lora_linear_attn_bwd; 0 for an invalid desc. */
+size_t lora_linear_attn_workspace_size(const lora_attn_desc* desc);
+
+/* Backward: dQ, dK, dV (bf16, the shapes of Q, K, V) from dO (bf16) and the
+ * forward's O and lse.  The gradients of shared key / value heads are summed
+ * over their query heads in fp32 in a fixed order (no atomics): the same bits
+ * in every call.  slopes get no gradient (frozen).  p and ds are rounded to
+ * bf16 for their products.
+ * workspace >= lora_linear_attn_workspace_size(desc) bytes. */
+lora_status_t lora_linear_attn_bwd(const lora_attn_desc* desc, void* plan, size_t plan_bytes, const void* dO,
+                                   const void* Q, const void* K, const void* V, const void* O, const float* lse,
+                                   const float* slopes, void* dQ, void* dK, void* dV, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -50,7 +50,10 @@ EXPORTED = ("lora_linear_workspace_size", "lora_linear_workspace_init", "lora_li
             "lora_linear_w4_tiled_bytes", "lora_linear_w4_tile", "lora_linear_fwd_w4_tiled",
             "lora_linear_rmsnorm_fwd", "lora_linear_rmsnorm_bwd", "lora_linear_workspace_size_rope",
             "lora_linear_fwd_rope", "lora_linear_bwd_rope", "lora_linear_ce_workspace_size",
-            "lora_linear_ce_fwd", "lora_linear_ce_bwd", "lora_linear_ce_fwd_bwd")
+            "lora_linear_ce_fwd", "lora_linear_ce_bwd", "lora_linear_ce_fwd_bwd",
+            "lora_linear_layernorm_fwd", "lora_linear_layernorm_workspace_size", "lora_linear_layernorm_bwd",
+            "lora_linear_rotary_tables", "lora_linear_rotary", "lora_linear_attn_plan_size", "lora_linear_attn_plan",
+            "lora_linear_attn_fwd", "lora_linear_attn_workspace_size", "lora_linear_attn_bwd")
 
 
 class LoraLinearDesc(ctypes.Structure):
@@ -67,6 +70,27 @@ class LoraRopeDesc(ctypes.Structure):
 class LoraCeDesc(ctypes.Structure):
     """Output projection + cross-entropy: M tokens, hidden size d, vocabulary V."""
     _fields_ = [("M", ctypes.c_int64), ("d", ctypes.c_int64), ("V", ctypes.c_int64)]
+
+
+class LoraRotaryTableDesc(ctypes.Structure):
+    """Rotary tables of a (stretched) context; scaling is one of ROTARY_SCALINGS."""
+    _fields_ = [("n_pos", ctypes.c_int64), ("rot", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("original", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class LoraRotaryDesc(ctypes.Structure):
+    """Rotation of finished q and k: the first rot features of each head."""
+    _fields_ = [("M", ctypes.c_int64), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inverse", ctypes.c_int32)]
+
+
+class LoraAttnDesc(ctypes.Structure):
+    """Attention over packed documents: M rows, n_docs documents."""
+    _fields_ = [("M", ctypes.c_int64), ("n_docs", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("softcap", ctypes.c_float)]
 
 
 class LoraError(RuntimeError):
@@ -150,6 +174,27 @@ def _load():
     lib.lora_linear_ce_bwd.restype = i32
     lib.lora_linear_ce_fwd_bwd.argtypes = [cp] + [vp] * 7 + [vp, sz, vp]
     lib.lora_linear_ce_fwd_bwd.restype = i32
+    lib.lora_linear_layernorm_fwd.argtypes = [vp, vp, vp, i64, i64, f32, vp, vp, vp, vp]
+    lib.lora_linear_layernorm_fwd.restype = i32
+    lib.lora_linear_layernorm_workspace_size.argtypes = [i64, i64]
+    lib.lora_linear_layernorm_workspace_size.restype = sz
+    lib.lora_linear_layernorm_bwd.argtypes = [vp, i32, vp, vp, vp, vp, i64, i64, vp, vp, vp, vp, sz, vp]
+    lib.lora_linear_layernorm_bwd.restype = i32
+    lib.lora_linear_rotary_tables.argtypes = [ctypes.POINTER(LoraRotaryTableDesc), vp, vp, vp]
+    lib.lora_linear_rotary_tables.restype = i32
+    lib.lora_linear_rotary.argtypes = [ctypes.POINTER(LoraRotaryDesc), rp, vp, vp, vp, vp, vp, sz, vp]
+    lib.lora_linear_rotary.restype = i32
+    lib.lora_linear_attn_plan_size.argtypes = [i64, i64]
+    lib.lora_linear_attn_plan_size.restype = sz
+    lib.lora_linear_attn_plan.argtypes = [vp, vp, i64, i64, i32, vp, sz, vp]
+    lib.lora_linear_attn_plan.restype = i32
+    ap = ctypes.POINTER(LoraAttnDesc)
+    lib.lora_linear_attn_fwd.argtypes = [ap, vp, sz] + [vp] * 7
+    lib.lora_linear_attn_fwd.restype = i32
+    lib.lora_linear_attn_workspace_size.argtypes = [ap]
+    lib.lora_linear_attn_workspace_size.restype = sz
+    lib.lora_linear_attn_bwd.argtypes = [ap, vp, sz] + [vp] * 11 + [sz, vp]
+    lib.lora_linear_attn_bwd.restype = i32
     return lib
 
 
@@ -523,3 +568,273 @@ def linear_cross_entropy_fwd_bwd(H, W, labels, dloss, workspace=None, stream=Non
                                   _ptr(lse), _ptr(dH), ws.buf.data_ptr(), ws.nbytes, _stream_handle(stream)),
            "lora_linear_ce_fwd_bwd")
     return loss, lse, dH
+
+
+# ---------------------------------------------------------------------------
+# layer norm, rotary positions, attention over packed documents
+# ---------------------------------------------------------------------------
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "wavelength": 3, "ramp": 4}
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def lora_linear_layernorm_fwd(X, g, b, M, d, eps, Y, mean, rstd, stream) -> int:
+    return int(_lib.lora_linear_layernorm_fwd(X, g, b, int(M), int(d), float(eps), Y, mean, rstd, stream))
+
+
+def lora_linear_layernorm_workspace_size(M, d) -> int:
+    return int(_lib.lora_linear_layernorm_workspace_size(int(M), int(d)))
+
+
+def lora_linear_layernorm_bwd(dY, dy_f32, X, g, mean, rstd, M, d, dX, dg, db, workspace, workspace_bytes,
+                              stream) -> int:
+    return int(_lib.lora_linear_layernorm_bwd(dY, int(dy_f32), X, g, mean, rstd, int(M), int(d), dX, dg, db, workspace,
+                                              workspace_bytes, stream))
+
+
+def make_rotary_table_desc(n_pos, rot, base=10000.0, scaling="none", factor=1.0, low=1.0, high=4.0, original=8192,
+                           amplitude=1.0) -> LoraRotaryTableDesc:
+    return LoraRotaryTableDesc(int(n_pos), int(rot), ROTARY_SCALINGS.get(scaling, scaling), float(base),
+                               float(factor), float(low), float(high), float(original), float(amplitude))
+
+
+def lora_linear_rotary_tables(desc, cos, sin, stream) -> int:
+    return int(_lib.lora_linear_rotary_tables(ctypes.byref(desc), cos, sin, stream))
+
+
+def make_rotary_desc(M, heads, kv_heads, head_dim, rot, layout="half", inverse=False) -> LoraRotaryDesc:
+    return LoraRotaryDesc(int(M), int(heads), int(kv_heads), int(head_dim), int(rot),
+                          ROTARY_LAYOUTS.get(layout, layout), int(inverse))
+
+
+def lora_linear_rotary(desc, rope, Q, K, Yq, Yk, workspace, workspace_bytes, stream) -> int:
+    """rope: make_rope_desc(pos, cos, sin, n_pos, head_dim), tables of rot / 2 columns."""
+    return int(_lib.lora_linear_rotary(ctypes.byref(desc), ctypes.byref(rope), Q, K, Yq, Yk, workspace,
+                                       workspace_bytes, stream))
+
+
+def lora_linear_attn_plan_size(M, n_docs) -> int:
+    return int(_lib.lora_linear_attn_plan_size(int(M), int(n_docs)))
+
+
+def lora_linear_attn_plan(starts, prefix_len, M, n_docs, causal, plan, plan_bytes, stream) -> int:
+    return int(_lib.lora_linear_attn_plan(starts, prefix_len, int(M), int(n_docs), int(causal), plan, plan_bytes,
+                                          stream))
+
+
+def make_attn_desc(M, n_docs, heads, kv_heads, head_dim, causal=True, scale=None, softcap=0.0) -> LoraAttnDesc:
+    """scale None: 1 / sqrt(head_dim)."""
+    return LoraAttnDesc(int(M), int(n_docs), int(heads), int(kv_heads), int(head_dim), int(causal),
+                        float(head_dim) ** -0.5 if scale is None else float(scale), float(softcap))
+
+
+def lora_linear_attn_fwd(desc, plan, plan_bytes, Q, K, V, slopes, O, lse, stream) -> int:
+    return int(_lib.lora_linear_attn_fwd(ctypes.byref(desc), plan, plan_bytes, Q, K, V, slopes, O, lse, stream))
+
+
+def lora_linear_attn_workspace_size(desc) -> int:
+    return int(_lib.lora_linear_attn_workspace_size(ctypes.byref(desc)))
+
+
+def lora_linear_attn_bwd(desc, plan, plan_bytes, dO, Q, K, V, O, lse, slopes, dQ, dK, dV, workspace, workspace_bytes,
+                         stream) -> int:
+    return int(_lib.lora_linear_attn_bwd(ctypes.byref(desc), plan, plan_bytes, dO, Q, K, V, O, lse, slopes, dQ, dK, dV,
+                                         workspace, workspace_bytes, stream))
+
+
+def _need(ok, what):
+    if not ok:
+        raise LoraError(1, what)
+
+
+def _tensors(device, named):
+    """Checks {name: (tensor or None, dtype, shape)}: device, type, shape, density.  A dimension of None is any."""
+    for name, (t, dtype, shape) in named.items():
+        if t is None:
+            continue
+        _need(t.device == device, f"{name} is on {t.device}, not {device}")
+        _need(t.dtype == dtype, f"{name} is {t.dtype}, not {dtype}")
+        _need(t.dim() == len(shape) and all(w is None or n == w for n, w in zip(t.shape, shape)),
+              f"{name} has shape {tuple(t.shape)}, not {shape}")
+        _need(t.is_contiguous(), f"{name} is not contiguous")
+
+
+class _On:
+    """The device of a call's tensors and its stream (None: that device's
+    current stream) as the current ones, so that outputs belong to the stream
+    that writes them; the inputs are recorded on a stream of the caller's."""
+
+    def __init__(self, device, stream, *inputs):
+        import torch
+        _need(device.type == "cuda", f"the tensors are on {device}, not on a CUDA device")
+        if stream is not None:
+            _need(stream.device == device, f"the stream is on {stream.device}, not {device}")
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(stream)
+        self._ctx = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self._ctx.__enter__()
+        return _stream_handle()
+
+    def __exit__(self, *exc):
+        return self._ctx.__exit__(*exc)
+
+
+def _workspace(workspace, nbytes, device):
+    if workspace is None:
+        return Workspace(nbytes, device)
+    _need(workspace.buf.device == device, f"the workspace is on {workspace.buf.device}, not {device}")
+    return workspace.ensure(nbytes)
+
+
+def layer_norm(X, g, b=None, eps=1e-5, stream=None):
+    """(Y, mean, rstd): the layer norm of each row of X (bf16 [M x d]) with
+    scale g and shift b (bf16 [d]; b may be None); mean, rstd fp32 [M] are the
+    backward's inputs."""
+    import torch
+    _need(X.dim() == 2, f"X has shape {tuple(X.shape)}")
+    M, d = X.shape
+    bf16, f32 = torch.bfloat16, torch.float32
+    _tensors(X.device, {"X": (X, bf16, (M, d)), "g": (g, bf16, (d,)), "b": (b, bf16, (d,))})
+    with _On(X.device, stream, X, g, b) as st:
+        Y = torch.empty_like(X)
+        mean, rstd = (torch.empty(M, dtype=f32, device=X.device) for _ in range(2))
+        _check(lora_linear_layernorm_fwd(_ptr(X), _ptr(g), _ptr(b), M, d, eps, _ptr(Y), _ptr(mean), _ptr(rstd), st),
+               "lora_linear_layernorm_fwd")
+    return Y, mean, rstd
+
+
+def layer_norm_backward(dY, X, g, mean, rstd, bias=True, workspace=None, stream=None):
+    """(dX, dg, db) for dY bf16 or fp32 [M x d]; dg, db fp32 [d] (db None
+    without ``bias``)."""
+    import torch
+    _need(X.dim() == 2, f"X has shape {tuple(X.shape)}")
+    M, d = X.shape
+    bf16, f32 = torch.bfloat16, torch.float32
+    _need(dY.dtype in (bf16, f32), f"dY is {dY.dtype}, not bfloat16 or float32")
+    _tensors(X.device, {"dY": (dY, dY.dtype, (M, d)), "X": (X, bf16, (M, d)), "g": (g, bf16, (d,)),
+                        "mean": (mean, f32, (M,)), "rstd": (rstd, f32, (M,))})
+    with _On(X.device, stream, dY, X, g, mean, rstd) as st:
+        dX = torch.empty_like(X)
+        dg = torch.empty(d, dtype=f32, device=X.device)
+        db = torch.empty(d, dtype=f32, device=X.device) if bias else None
+        ws = _workspace(workspace, lora_linear_layernorm_workspace_size(M, d), X.device)
+        _check(lora_linear_layernorm_bwd(_ptr(dY), dY.dtype == f32, _ptr(X), _ptr(g), _ptr(mean), _ptr(rstd), M, d,
+                                         _ptr(dX), _ptr(dg), _ptr(db), ws.buf.data_ptr(), ws.nbytes, st),
+               "lora_linear_layernorm_bwd")
+    return dX, dg, db
+
+
+def rotary_tables(n_pos, rot, base=10000.0, scaling="none", factor=1.0, low=1.0, high=4.0, original=8192,
+                  amplitude=1.0, device=None, stream=None):
+    """(cos, sin) fp32 [n_pos x rot/2] on ``device`` (default: the current one)
+    under a scaling of ROTARY_SCALINGS; low and high are numbers of turns over
+    the ``original`` context ("wavelength", "ramp")."""
+    import torch
+    _need(scaling in ROTARY_SCALINGS, f"scaling {scaling!r} is none of {sorted(ROTARY_SCALINGS)}")
+    _need(n_pos >= 0 and rot >= 0, f"n_pos {n_pos}, rot {rot}")
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device()) if stream is None else stream.device
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    desc = make_rotary_table_desc(n_pos, rot, base, scaling, factor, low, high, original, amplitude)
+    with _On(device, stream) as st:
+        cos, sin = (torch.empty((n_pos, rot // 2), dtype=torch.float32, device=device) for _ in range(2))
+        _check(lora_linear_rotary_tables(desc, _ptr(cos), _ptr(sin), st), "lora_linear_rotary_tables")
+    return cos, sin
+
+
+def rotary(Q, K, pos, cos, sin, head_dim, layout="half", inverse=False, inplace=False, workspace=None, stream=None):
+    """(Yq, Yk): the heads of Q [M x heads * head_dim] and K (bf16; K may be
+    None) turned at the int32 positions pos [M] by the tables cos, sin
+    [n_pos x rot/2]; the first rot features of each head take part.
+    ``inverse`` turns back: the gradients of Q and K from those of Yq and Yk."""
+    import torch
+    _need(layout in ROTARY_LAYOUTS, f"layout {layout!r} is none of {sorted(ROTARY_LAYOUTS)}")
+    _need(Q.dim() == 2 and cos.dim() == 2, f"Q has shape {tuple(Q.shape)}, cos {tuple(cos.shape)}")
+    M, n_pos, rot = Q.shape[0], cos.shape[0], 2 * cos.shape[1]
+    _need(head_dim > 0 and Q.shape[1] % head_dim == 0, f"{Q.shape[1]} features are no heads of {head_dim}")
+    _need(K is None or (K.dim() == 2 and K.shape[1] % head_dim == 0), f"K's features are no heads of {head_dim}")
+    bf16, f32 = torch.bfloat16, torch.float32
+    _tensors(Q.device, {"Q": (Q, bf16, (M, None)), "K": (K, bf16, (M, None)), "pos": (pos, torch.int32, (M,)),
+                        "cos": (cos, f32, (n_pos, rot // 2)), "sin": (sin, f32, (n_pos, rot // 2))})
+    desc = make_rotary_desc(M, Q.shape[1] // head_dim, 0 if K is None else K.shape[1] // head_dim, head_dim, rot,
+                            layout, inverse)
+    rope = make_rope_desc(_ptr(pos), _ptr(cos), _ptr(sin), n_pos, head_dim)
+    with _On(Q.device, stream, Q, K, pos, cos, sin) as st:
+        Yq = Q if inplace else torch.empty_like(Q)
+        Yk = K if inplace or K is None else torch.empty_like(K)
+        ws = _workspace(workspace, 256, Q.device)
+        _check(lora_linear_rotary(desc, rope, _ptr(Q), _ptr(K), _ptr(Yq), _ptr(Yk), ws.buf.data_ptr(), ws.nbytes, st),
+               "lora_linear_rotary")
+    return Yq, Yk
+
+
+class AttentionPlan:
+    """The documents of a batch of M rows as tiles, for ``attention`` and
+    ``attention_backward`` of every layer: starts (int32 [n_docs + 1], on the
+    GPU) holds the documents' first rows and the end of the last one.  Without
+    ``causal`` a row sees its whole document, with it the rows up to itself and
+    the first prefix_len (int32 [n_docs]) rows of its document.  status() is 2
+    if the offsets were not valid."""
+
+    def __init__(self, starts, M, prefix_len=None, causal=True, stream=None):
+        import torch
+        _need(starts.dim() == 1 and starts.numel() >= 1, f"starts has shape {tuple(starts.shape)}")
+        n = starts.numel() - 1
+        _tensors(starts.device, {"starts": (starts, torch.int32, (n + 1,)), "prefix_len": (prefix_len, torch.int32, (n,))})
+        self.M, self.n_docs, self.causal, self.nbytes = int(M), n, bool(causal), lora_linear_attn_plan_size(M, n)
+        _need(self.nbytes > 0, f"{M} rows in {n} documents")
+        with _On(starts.device, stream, starts, prefix_len) as st:
+            self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=starts.device)
+            _check(lora_linear_attn_plan(_ptr(starts), _ptr(prefix_len), self.M, n, self.causal, self.buf.data_ptr(),
+                                         self.nbytes, st), "lora_linear_attn_plan")
+
+    def status(self, stream=None):
+        return lora_linear_device_status(self.buf.data_ptr(), _stream_handle(stream))[1]
+
+
+def _attention_args(Q, K, V, plan, heads, kv_heads, scale, softcap, slopes, more):
+    import torch
+    _need(Q.dim() == 2 and heads > 0 and kv_heads > 0 and Q.shape[1] % heads == 0,
+          f"Q has shape {tuple(Q.shape)} for {heads} heads")
+    M, D, bf16 = Q.shape[0], Q.shape[1] // heads, torch.bfloat16
+    _need(M == plan.M, f"{M} rows with a plan of {plan.M}")
+    _tensors(Q.device, {"Q": (Q, bf16, (M, heads * D)), "K": (K, bf16, (M, kv_heads * D)),
+                        "V": (V, bf16, (M, kv_heads * D)), "slopes": (slopes, torch.float32, (heads,)),
+                        "the plan": (plan.buf, torch.uint8, (plan.nbytes,))} | more(M, D))
+    return make_attn_desc(M, plan.n_docs, heads, kv_heads, D, plan.causal, scale, softcap)
+
+
+def attention(Q, K, V, plan, heads, kv_heads, scale=None, softcap=0.0, slopes=None, stream=None):
+    """(O, lse): attention of Q (bf16 [M x heads * head_dim]) over K, V (bf16
+    [M x kv_heads * head_dim]) within the plan's documents; scale None is
+    1 / sqrt(head_dim), softcap caps the scores by a tanh, slopes (fp32
+    [heads]) subtract slope * |i - j|.  lse fp32 [M x heads] is the backward's
+    input."""
+    import torch
+    desc = _attention_args(Q, K, V, plan, heads, kv_heads, scale, softcap, slopes, lambda M, D: {})
+    with _On(Q.device, stream, Q, K, V, slopes, plan.buf) as st:
+        O = torch.empty_like(Q)
+        lse = torch.empty((Q.shape[0], heads), dtype=torch.float32, device=Q.device)
+        _check(lora_linear_attn_fwd(desc, plan.buf.data_ptr(), plan.nbytes, _ptr(Q), _ptr(K), _ptr(V), _ptr(slopes),
+                                    _ptr(O), _ptr(lse), st), "lora_linear_attn_fwd")
+    return O, lse
+
+
+def attention_backward(dO, Q, K, V, O, lse, plan, heads, kv_heads, scale=None, softcap=0.0, slopes=None,
+                       workspace=None, stream=None):
+    """(dQ, dK, dV) of ``attention`` for its O and lse."""
+    import torch
+    desc = _attention_args(Q, K, V, plan, heads, kv_heads, scale, softcap, slopes, lambda M, D: {
+        "dO": (dO, torch.bfloat16, (M, heads * D)), "O": (O, torch.bfloat16, (M, heads * D)),
+        "lse": (lse, torch.float32, (M, heads))})
+    with _On(Q.device, stream, dO, Q, K, V, O, lse, slopes, plan.buf) as st:
+        dQ, dK, dV = torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V)
+        ws = _workspace(workspace, lora_linear_attn_workspace_size(desc), Q.device)
+        _check(lora_linear_attn_bwd(desc, plan.buf.data_ptr(), plan.nbytes, _ptr(dO), _ptr(Q), _ptr(K), _ptr(V),
+                                    _ptr(O), _ptr(lse), _ptr(slopes), _ptr(dQ), _ptr(dK), _ptr(dV),
+                                    ws.buf.data_ptr(), ws.nbytes, st), "lora_linear_attn_bwd")
+    return dQ, dK, dV

@@ -1,0 +1,296 @@
+// lora_attention.cuh — attention over packed documents, forward and backward.
+//
+//   z_ij = cap tanh(scale q_i.k_j / cap) - slope |i - j|     (no cap: scale q_i.k_j; no slopes: no bias)
+//   p_ij = exp(z_ij - lse_i),  lse_i = log sum_j exp z_ij,  o_i = sum_j p_ij v_j
+// over the keys j that row i sees: those of its own document with j <= i or
+// j before the end of the document's prefix.
+//   delta_i = do_i.o_i,  dz_ij = p_ij (do_i.v_j - delta_i)
+//   ds_ij = scale dz_ij (1 - tanh^2),  dq_i = sum_j ds_ij k_j,  dk_j = sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i
+#pragma once
+
+#include "lora_norm_rope.cuh"
+
+namespace lora {
+
+// ---------------------------------------------------------------------------
+// the plan: the documents of a batch as lists of tiles
+// ---------------------------------------------------------------------------
+// A tile is up to kAttnTile (the forward: 2 kAttnTile) rows of one document.
+// Tiles start at the document's first row, so a tile never holds rows of two
+// documents and whatever a document's rows hold stays out of its neighbours.
+// Rows behind the last document come as tiles of their own (prefix_end < 0),
+// whose outputs are zero.
+constexpr int kAttnTile = 128;
+
+struct AttnTileRef {
+  int row0;          // first row
+  int begin, end;    // the document's rows
+  int prefix_end;    // first row past the document's prefix; -1: rows behind the last document
+};
+
+// The plan's header, words of 4 bytes (word 0 is the status word).
+enum : int {
+  kPlanM = 16,           // rows the plan was made for
+  kPlanDocs = 17,
+  kPlanFwd = 18,         // tiles in each list
+  kPlanQ = 19,
+  kPlanKv = 20,
+};
+
+struct AttnPlanView {
+  uint32_t* head;
+  AttnTileRef* fwd;      // 2 kAttnTile query rows
+  AttnTileRef* q;        // kAttnTile query rows
+  AttnTileRef* kv;       // kAttnTile key rows
+  int max_fwd, max_q;    // capacities (kv: as q)
+};
+
+constexpr int kPlanBuckets = 1024;
+
+// Visits the tiles of every list: f(list, work, tile), work in key (list kv:
+// query) tiles of kAttnTile.  A warp takes a document, its lanes the tiles.
+template <typename F>
+__device__ __forceinline__ void plan_tiles(const int* starts, const int* prefix, int M, int n_docs, int causal, F f) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarp = blockDim.x >> 5;
+  for (int d = warp; d <= n_docs; d += nwarp) {
+    const bool behind = d == n_docs;
+    const int a = starts[d], e = behind ? M : starts[d + 1];
+    const int len = e - a;
+    if (len <= 0) continue;
+    const int pre = behind ? -1 : a + (causal ? (prefix != nullptr ? prefix[d] : 0) : len);
+    const int tiles = (len + kAttnTile - 1) / kAttnTile;
+    for (int t = lane; t < tiles; t += 32) {
+      const int r0 = a + t * kAttnTile;
+      const AttnTileRef ref{r0, a, e, pre};
+      if (behind) {
+        if (t % 2 == 0) f(0, 0, ref);
+        f(1, 0, ref);
+        f(2, 0, ref);
+        continue;
+      }
+      auto keys = [&](int rows) {
+        int last = r0 + rows < e ? r0 + rows : e;
+        last = last > pre ? last : pre;
+        return (last - a + kAttnTile - 1) / kAttnTile;
+      };
+      if (t % 2 == 0) f(0, keys(2 * kAttnTile), ref);
+      f(1, keys(kAttnTile), ref);
+      f(2, r0 < pre ? tiles : tiles - t, ref);
+    }
+  }
+}
+
+// One CTA.  Lists the tiles in falling order of their work (a counting sort,
+// work above the last bucket together), so that the tiles handed out last are
+// short.  Offsets that do not rise from 0 to at most M, or a prefix longer
+// than its document, set the status bit and leave the lists empty.
+__global__ void __launch_bounds__(1024)
+    attn_plan_kernel(const int* __restrict__ starts, const int* __restrict__ prefix, int M, int n_docs, int causal,
+                     AttnPlanView v) {
+  __shared__ int count[3][kPlanBuckets];
+  __shared__ int bad;
+  grid_dep_wait();
+  if (threadIdx.x == 0) bad = 0;
+  for (int i = threadIdx.x; i < 3 * kPlanBuckets; i += blockDim.x) (&count[0][0])[i] = 0;
+  __syncthreads();
+  bool b = false;
+  for (int d = threadIdx.x; d <= n_docs; d += blockDim.x) {
+    const int a = starts[d];
+    if (a < 0 || a > M || (d == 0 && a != 0)) b = true;
+    if (d < n_docs) {
+      const int e = starts[d + 1];
+      if (e < a || e > M) b = true;
+      else if (causal && prefix != nullptr && (prefix[d] < 0 || prefix[d] > e - a)) b = true;
+    }
+  }
+  if (b) bad = 1;
+  __syncthreads();
+  const bool good = bad == 0;
+  if (threadIdx.x == 0) {
+    v.head[0] = good ? 0u : static_cast<uint32_t>(kStatusBadArgument);
+    v.head[kPlanM] = static_cast<uint32_t>(M);
+    v.head[kPlanDocs] = static_cast<uint32_t>(n_docs);
+    if (!good) v.head[kPlanFwd] = v.head[kPlanQ] = v.head[kPlanKv] = 0u;
+  }
+  if (!good) return;
+  auto bucket = [](int work) { return kPlanBuckets - 1 - (work < kPlanBuckets ? work : kPlanBuckets - 1); };
+  plan_tiles(starts, prefix, M, n_docs, causal,
+             [&](int list, int work, const AttnTileRef&) { atomicAdd(&count[list][bucket(work)], 1); });
+  __syncthreads();
+  // exclusive sums over the buckets, one warp a list
+  if (threadIdx.x < 96) {
+    const int list = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int run = 0;
+    for (int i0 = 0; i0 < kPlanBuckets; i0 += 32) {
+      const int c = count[list][i0 + lane];
+      int s = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += t;
+      }
+      count[list][i0 + lane] = run + s - c;
+      run += __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (lane == 0) v.head[kPlanFwd + list] = static_cast<uint32_t>(run);
+  }
+  __syncthreads();
+  AttnTileRef* lists[3] = {v.fwd, v.q, v.kv};
+  plan_tiles(starts, prefix, M, n_docs, causal, [&](int list, int work, const AttnTileRef& ref) {
+    lists[list][atomicAdd(&count[list][bucket(work)], 1)] = ref;
+  });
+}
+
+// ---------------------------------------------------------------------------
+// kernels
+// ---------------------------------------------------------------------------
+struct AttnParams {
+  AttnPlanView plan;
+  const __nv_bfloat16 *Q, *K, *V, *dO;
+  const float* slopes;           // [heads] or null
+  __nv_bfloat16 *O, *dQ, *dK, *dV;
+  float *lse, *delta;            // [M x heads]
+  int M, n_docs, heads, kv_heads;
+  float scale, cap;              // cap 0: none
+};
+
+__device__ __forceinline__ bool attn_plan_ok(const AttnParams& p) {
+  if (p.plan.head[kPlanM] == static_cast<uint32_t>(p.M) && p.plan.head[kPlanDocs] == static_cast<uint32_t>(p.n_docs))
+    return true;
+  atomicOr(p.plan.head, static_cast<uint32_t>(kStatusBadArgument));
+  return false;
+}
+
+// One warp a row and head, the head's features spread over the lanes.
+template <int D>
+struct AttnRow {
+  static constexpr int n = D / 32;
+  float v[n];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = __bfloat162float(p[(threadIdx.x & 31) + 32 * i]);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+#pragma unroll
+    for (int i = 0; i < n; ++i) p[(threadIdx.x & 31) + 32 * i] = __float2bfloat16_rn(v[i]);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = 0.0f;
+  }
+  __device__ __forceinline__ float dot(const AttnRow& o) const {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < n; ++i) s = fmaf(v[i], o.v[i], s);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    return s;
+  }
+  __device__ __forceinline__ void add(float a, const AttnRow& o) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = fmaf(a, o.v[i], v[i]);
+  }
+};
+
+// z, and d z / d (scale q.k) in *slope_z.
+__device__ __forceinline__ float attn_score(const AttnParams& p, float qk, int h, int i, int j, float* dz) {
+  float z = qk * p.scale;
+  *dz = 1.0f;
+  if (p.cap > 0.0f) {
+    const float t = tanhf(z / p.cap);
+    z = p.cap * t;
+    *dz = 1.0f - t * t;
+  }
+  if (p.slopes != nullptr) z -= p.slopes[h] * fabsf(static_cast<float>(i - j));
+  return z;
+}
+
+// kind 0: o, lse; 1: delta and dq.  grid: tile x heads, 4 warps.
+template <int D, int kind>
+__global__ void __launch_bounds__(128) attn_rows_kernel(const __grid_constant__ AttnParams p) {
+  grid_dep_wait();
+  if (!attn_plan_ok(p) || blockIdx.x >= p.plan.head[kPlanQ]) return;
+  const AttnTileRef t = p.plan.q[blockIdx.x];
+  const int h = blockIdx.y, hk = h / (p.heads / p.kv_heads), lane = threadIdx.x & 31;
+  const size_t qs = static_cast<size_t>(p.heads) * D, ks = static_cast<size_t>(p.kv_heads) * D;
+  const int last = t.row0 + kAttnTile < t.end ? t.row0 + kAttnTile : t.end;
+  for (int i = t.row0 + (threadIdx.x >> 5); i < last; i += 4) {
+    const size_t at = i * qs + static_cast<size_t>(h) * D, st = static_cast<size_t>(i) * p.heads + h;
+    AttnRow<D> q, o, k, v, g;
+    o.zero();
+    const bool behind = t.prefix_end < 0;
+    const int hi = behind ? t.begin : (i + 1 > t.prefix_end ? i + 1 : t.prefix_end);
+    float m = -INFINITY, l = 0.0f, dz;
+    if (!behind) q.load(p.Q + at);
+    if constexpr (kind == 0) {
+      for (int j = t.begin; j < hi; ++j) {
+        k.load(p.K + j * ks + static_cast<size_t>(hk) * D);
+        v.load(p.V + j * ks + static_cast<size_t>(hk) * D);
+        const float z = attn_score(p, q.dot(k), h, i, j, &dz);
+        const float mn = fmaxf(m, z), a = expf(m - mn), e = expf(z - mn);
+        l = l * a + e;
+#pragma unroll
+        for (int c = 0; c < o.n; ++c) o.v[c] *= a;
+        o.add(e, v);
+        m = mn;
+      }
+      if (l > 0.0f)
+#pragma unroll
+        for (int c = 0; c < o.n; ++c) o.v[c] /= l;
+      o.store(p.O + at);
+      if (lane == 0) p.lse[st] = behind ? -INFINITY : m + logf(l);
+    } else {
+      float delta = 0.0f;
+      if (!behind) {
+        g.load(p.dO + at);
+        k.load(p.O + at);
+        delta = g.dot(k);
+      }
+      for (int j = t.begin; j < hi; ++j) {
+        k.load(p.K + j * ks + static_cast<size_t>(hk) * D);
+        v.load(p.V + j * ks + static_cast<size_t>(hk) * D);
+        const float z = attn_score(p, q.dot(k), h, i, j, &dz);
+        const float e = expf(z - p.lse[st]);
+        o.add(p.scale * e * (g.dot(v) - delta) * dz, k);
+      }
+      o.store(p.dQ + at);
+      if (lane == 0) p.delta[st] = delta;
+    }
+  }
+}
+
+// dk, dv.  grid: tile x kv heads, 4 warps.
+template <int D>
+__global__ void __launch_bounds__(128) attn_keys_kernel(const __grid_constant__ AttnParams p) {
+  grid_dep_wait();
+  if (!attn_plan_ok(p) || blockIdx.x >= p.plan.head[kPlanKv]) return;
+  const AttnTileRef t = p.plan.kv[blockIdx.x];
+  const int hk = blockIdx.y, n = p.heads / p.kv_heads;
+  const size_t qs = static_cast<size_t>(p.heads) * D, ks = static_cast<size_t>(p.kv_heads) * D;
+  const int last = t.row0 + kAttnTile < t.end ? t.row0 + kAttnTile : t.end;
+  for (int j = t.row0 + (threadIdx.x >> 5); j < last; j += 4) {
+    const size_t at = j * ks + static_cast<size_t>(hk) * D;
+    AttnRow<D> q, g, k, v, dk, dv;
+    dk.zero();
+    dv.zero();
+    if (t.prefix_end >= 0) {
+      k.load(p.K + at);
+      v.load(p.V + at);
+      for (int h = hk * n; h < (hk + 1) * n; ++h)
+        for (int i = j < t.prefix_end ? t.begin : j; i < t.end; ++i) {
+          q.load(p.Q + i * qs + static_cast<size_t>(h) * D);
+          g.load(p.dO + i * qs + static_cast<size_t>(h) * D);
+          const size_t st = static_cast<size_t>(i) * p.heads + h;
+          float dz;
+          const float z = attn_score(p, q.dot(k), h, i, j, &dz);
+          const float e = expf(z - p.lse[st]);
+          dv.add(e, g);
+          dk.add(p.scale * e * (g.dot(v) - p.delta[st]) * dz, q);
+        }
+    }
+    dk.store(p.dK + at);
+    dv.store(p.dV + at);
+  }
+}
+
+}  // namespace lora

@@ -24,6 +24,9 @@
 #include "lora_dropout.cuh"
 #include "lora_norm_rope.cuh"
 #include "lora_ce.cuh"
+#include "lora_layernorm.cuh"
+#include "lora_rotary.cuh"
+#include "lora_attention.cuh"
 
 namespace {
 
@@ -2074,6 +2077,382 @@ lora_status_t lora_linear_ce_fwd_bwd(const lora_ce_desc* d, const void* H, const
   launch_k(ce_mean_kernel, dim3(1), dim3(kCeMeanThreads), 0, st, false, static_cast<const float*>(loss_tok), labels,
            static_cast<int>(M), static_cast<int>(V), loss);
   return check_launch("ce_mean_kernel");
+}
+
+}  // extern "C"
+
+// ===========================================================================
+// layer norm (lora_layernorm.cuh), rotary positions (lora_rotary.cuh) and
+// attention over packed documents (lora_attention.cuh)
+// ===========================================================================
+namespace {
+
+// Threads a row: the smallest group whose kLnNV chunks a thread hold d features.
+int ln_group(int64_t d) {
+  int t = 32;
+  while (static_cast<int64_t>(t) * 8 * kLnNV < d) t *= 2;
+  return t;
+}
+
+int ln_grid(int64_t M, int group, int per_sm, const DevInfo& dev) {
+  const int64_t blocks = ceil_div(M, group >= 256 ? 1 : 256 / group);
+  const int64_t cap = static_cast<int64_t>(dev.sms) * per_sm;
+  return static_cast<int>(blocks < cap ? blocks : cap);
+}
+
+// CTAs that stay for their rows in the backward: enough threads to fill the
+// SMs, and no more partial rows than that.
+constexpr int kLnBwdPerSm = 2;
+
+lora_status_t check_layernorm(const void* X, const void* g, int64_t M, int64_t d, const void* out, const float* mean,
+                              const float* rstd) {
+  if (M < 0 || d <= 0 || g == nullptr) return LORA_ERR_INVALID_ARG;
+  if (M > 0 && (X == nullptr || out == nullptr || mean == nullptr || rstd == nullptr)) return LORA_ERR_INVALID_ARG;
+  if (d % 8 != 0 || !aligned16(g) || !aligned16(X) || !aligned16(out) || !aligned4(mean) || !aligned4(rstd))
+    return LORA_ERR_ALIGNMENT;
+  if (d > kLnMaxD || M > (int64_t(1) << 40)) return LORA_ERR_UNSUPPORTED;
+  return LORA_OK;
+}
+
+template <int T>
+lora_status_t launch_ln_fwd(const void* X, const void* g, const void* b, int64_t M, int64_t d, float eps, void* Y,
+                            float* mean, float* rstd, const DevInfo& dev, cudaStream_t st) {
+  launch_k(layernorm_fwd_kernel<T>, dim3(ln_grid(M, T, 2048 / LnCfg<T>::kThreads, dev)), dim3(LnCfg<T>::kThreads), 0,
+           st, false, static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(g),
+           static_cast<const __nv_bfloat16*>(b), static_cast<long long>(M), static_cast<int>(d), eps,
+           static_cast<__nv_bfloat16*>(Y), mean, rstd);
+  return check_launch("layernorm_fwd_kernel");
+}
+
+template <int T, typename TDy>
+lora_status_t launch_ln_bwd(const void* dY, const void* X, const void* g, const float* mean, const float* rstd,
+                            int64_t M, int64_t d, void* dX, float* part, int grid, cudaStream_t st) {
+  const size_t smem = LnCfg<T>::kGroups > 1 ? static_cast<size_t>(2 * d) * 4 : 0;
+  launch_k(layernorm_bwd_kernel<T, TDy>, dim3(grid), dim3(LnCfg<T>::kThreads), smem, st, false,
+           static_cast<const TDy*>(dY), static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(g),
+           mean, rstd, static_cast<long long>(M), static_cast<int>(d), static_cast<__nv_bfloat16*>(dX), part);
+  return check_launch("layernorm_bwd_kernel");
+}
+
+#define LORA_LN_DISPATCH(group, call)      \
+  switch (group) {                         \
+    case 32: LORA_TRY(call(32)); break;    \
+    case 64: LORA_TRY(call(64)); break;    \
+    case 128: LORA_TRY(call(128)); break;  \
+    case 256: LORA_TRY(call(256)); break;  \
+    case 512: LORA_TRY(call(512)); break;  \
+    default: LORA_TRY(call(1024)); break;  \
+  }
+
+lora_status_t check_rotary_table(const lora_rotary_table_desc* d) {
+  if (d == nullptr || d->n_pos < 0 || d->scaling < LORA_ROTARY_PLAIN || d->scaling > LORA_ROTARY_RAMP)
+    return LORA_ERR_INVALID_ARG;
+  if (!std::isfinite(d->base) || d->base <= 1.0 || !std::isfinite(d->amplitude) || d->amplitude <= 0.0)
+    return LORA_ERR_INVALID_ARG;
+  if (d->scaling != LORA_ROTARY_PLAIN && (!std::isfinite(d->factor) || d->factor < 1.0)) return LORA_ERR_INVALID_ARG;
+  if (d->scaling >= LORA_ROTARY_WAVELENGTH &&
+      (!std::isfinite(d->low) || !std::isfinite(d->high) || !std::isfinite(d->original) || d->low <= 0.0 ||
+       d->high <= d->low || d->original <= 0.0))
+    return LORA_ERR_INVALID_ARG;
+  if (d->rot < 16 || d->rot > 2 * kRotaryMaxPairs || d->rot % 16 != 0 || d->n_pos > (int64_t(1) << 31))
+    return LORA_ERR_UNSUPPORTED;
+  return LORA_OK;
+}
+
+// Turns per position of each pair under the scaling.
+void rotary_turns(const lora_rotary_table_desc* d, RotaryTurns* out) {
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  const int pairs = d->rot / 2;
+  double base = d->base;
+  if (d->scaling == LORA_ROTARY_NTK) base *= std::pow(d->factor, static_cast<double>(d->rot) / (d->rot - 2));
+  double first = 0.0, last = 0.0;
+  if (d->scaling == LORA_ROTARY_RAMP) {
+    const double per = d->rot / (2.0 * std::log(base));
+    first = std::fmax(0.0, std::floor(per * std::log(d->original / (kTwoPi * d->high))));
+    last = std::fmin(d->rot - 1.0, std::ceil(per * std::log(d->original / (kTwoPi * d->low))));
+  }
+  for (int i = 0; i < pairs; ++i) {
+    double f = std::pow(base, -2.0 * i / d->rot);
+    double keep = 1.0;
+    if (d->scaling == LORA_ROTARY_LINEAR) keep = 0.0;
+    if (d->scaling == LORA_ROTARY_WAVELENGTH) keep = (d->original * f / kTwoPi - d->low) / (d->high - d->low);
+    if (d->scaling == LORA_ROTARY_RAMP) keep = 1.0 - (i - first) / std::fmax(last - first, 1e-3);
+    keep = std::fmin(1.0, std::fmax(0.0, keep));
+    if (d->scaling != LORA_ROTARY_PLAIN && d->scaling != LORA_ROTARY_NTK) f = f * keep + f / d->factor * (1.0 - keep);
+    out->w[i] = f / kTwoPi;
+  }
+}
+
+// Tile lists of a plan: byte offsets and capacities.
+struct AttnPlanLayout {
+  int64_t max_fwd = 0, max_q = 0;
+  size_t fwd = 0, q = 0, kv = 0, total = 0;
+};
+
+bool attn_plan_sizes_ok(int64_t M, int64_t n_docs) {
+  return M >= 0 && M <= (int64_t(1) << 30) && n_docs >= 0 && n_docs <= (int64_t(1) << 30);
+}
+
+AttnPlanLayout attn_plan_layout(int64_t M, int64_t n_docs) {
+  AttnPlanLayout L;
+  // every document, and the rows behind the last one, round up once
+  L.max_fwd = ceil_div(M, 2 * kAttnTile) + n_docs + 1;
+  L.max_q = ceil_div(M, kAttnTile) + n_docs + 1;
+  L.fwd = kHeaderBytes;
+  L.q = L.fwd + align_up(static_cast<size_t>(L.max_fwd) * sizeof(AttnTileRef), 256);
+  L.kv = L.q + align_up(static_cast<size_t>(L.max_q) * sizeof(AttnTileRef), 256);
+  L.total = L.kv + align_up(static_cast<size_t>(L.max_q) * sizeof(AttnTileRef), 256);
+  return L;
+}
+
+AttnPlanView attn_plan_view(void* plan, int64_t M, int64_t n_docs) {
+  const AttnPlanLayout L = attn_plan_layout(M, n_docs);
+  uint8_t* b = static_cast<uint8_t*>(plan);
+  AttnPlanView v;
+  v.head = reinterpret_cast<uint32_t*>(b);
+  v.fwd = reinterpret_cast<AttnTileRef*>(b + L.fwd);
+  v.q = reinterpret_cast<AttnTileRef*>(b + L.q);
+  v.kv = reinterpret_cast<AttnTileRef*>(b + L.kv);
+  v.max_fwd = static_cast<int>(L.max_fwd);
+  v.max_q = static_cast<int>(L.max_q);
+  return v;
+}
+
+lora_status_t check_attn_desc(const lora_attn_desc* d) {
+  if (d == nullptr || d->M < 0 || d->n_docs < 0 || d->heads < 1 || d->kv_heads < 1 || d->heads % d->kv_heads != 0 ||
+      (d->causal != 0 && d->causal != 1))
+    return LORA_ERR_INVALID_ARG;
+  if (!std::isfinite(d->scale) || d->scale <= 0.0f || !std::isfinite(d->softcap) || d->softcap < 0.0f)
+    return LORA_ERR_INVALID_ARG;
+  if (!attn_plan_sizes_ok(d->M, d->n_docs) || d->heads > 4096 || (d->head_dim != 64 && d->head_dim != 128))
+    return LORA_ERR_UNSUPPORTED;
+  return LORA_OK;
+}
+
+lora_status_t check_attn_plan(const lora_attn_desc* d, const void* plan, size_t plan_bytes) {
+  if (plan == nullptr || !aligned16(plan) || plan_bytes < attn_plan_layout(d->M, d->n_docs).total)
+    return LORA_ERR_WORKSPACE;
+  return LORA_OK;
+}
+
+AttnParams attn_params(const lora_attn_desc* d, void* plan, const void* Q, const void* K, const void* V,
+                       const float* slopes, float* lse) {
+  AttnParams p = {};
+  p.plan = attn_plan_view(plan, d->M, d->n_docs);
+  p.Q = static_cast<const __nv_bfloat16*>(Q);
+  p.K = static_cast<const __nv_bfloat16*>(K);
+  p.V = static_cast<const __nv_bfloat16*>(V);
+  p.slopes = slopes;
+  p.lse = lse;
+  p.M = static_cast<int>(d->M);
+  p.n_docs = static_cast<int>(d->n_docs);
+  p.heads = d->heads;
+  p.kv_heads = d->kv_heads;
+  p.scale = d->scale;
+  p.cap = d->softcap;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+lora_status_t lora_linear_layernorm_fwd(const void* X, const void* g, const void* b, int64_t M, int64_t d, float eps,
+                                        void* Y, float* mean, float* rstd, void* stream) {
+  LORA_TRY(check_layernorm(X, g, M, d, Y, mean, rstd));
+  if (!std::isfinite(eps) || eps < 0.0f) return LORA_ERR_INVALID_ARG;
+  if (!aligned16(b)) return LORA_ERR_ALIGNMENT;
+  DevInfo dev;
+  LORA_TRY(check_arch(&dev));
+  if (M == 0) return LORA_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+#define LORA_CALL(T) launch_ln_fwd<T>(X, g, b, M, d, eps, Y, mean, rstd, dev, st)
+  LORA_LN_DISPATCH(ln_group(d), LORA_CALL)
+#undef LORA_CALL
+  return LORA_OK;
+}
+
+size_t lora_linear_layernorm_workspace_size(int64_t M, int64_t d) {
+  if (M < 0 || M > (int64_t(1) << 40) || d <= 0 || d > kLnMaxD || d % 8 != 0) return 0;
+  const int group = ln_group(d);
+  const int64_t blocks = ceil_div(M, group >= 256 ? 1 : 256 / group);
+  const int64_t most = static_cast<int64_t>(kTargetCtas) * kLnBwdPerSm;
+  return kHeaderBytes + static_cast<size_t>(blocks < most ? blocks : most) * 2 * d * sizeof(float);
+}
+
+lora_status_t lora_linear_layernorm_bwd(const void* dY, int dy_f32, const void* X, const void* g, const float* mean,
+                                        const float* rstd, int64_t M, int64_t d, void* dX, float* dg, float* db,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  LORA_TRY(check_layernorm(X, g, M, d, dX, mean, rstd));
+  if ((dy_f32 != 0 && dy_f32 != 1) || (M > 0 && dY == nullptr)) return LORA_ERR_INVALID_ARG;
+  if (!aligned16(dY) || !aligned4(dg) || !aligned4(db)) return LORA_ERR_ALIGNMENT;
+  if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < lora_linear_layernorm_workspace_size(M, d))
+    return LORA_ERR_WORKSPACE;
+  DevInfo dev;
+  LORA_TRY(check_arch(&dev));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    if (dg != nullptr && cudaMemsetAsync(dg, 0, static_cast<size_t>(d) * 4, st) != cudaSuccess)
+      return cuda_error("cudaMemsetAsync(dg)");
+    if (db != nullptr && cudaMemsetAsync(db, 0, static_cast<size_t>(d) * 4, st) != cudaSuccess)
+      return cuda_error("cudaMemsetAsync(db)");
+    return LORA_OK;
+  }
+  DevInfo grid_dev = dev;
+  if (grid_dev.sms > kTargetCtas) grid_dev.sms = kTargetCtas;    // the workspace is sized without a device
+  const int group = ln_group(d), grid = ln_grid(M, group, kLnBwdPerSm, grid_dev);
+  float* part = dg != nullptr || db != nullptr
+                    ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes) : nullptr;
+#define LORA_CALL(T)                                                                                    \
+  (dy_f32 ? launch_ln_bwd<T, float>(dY, X, g, mean, rstd, M, d, dX, part, grid, st)                     \
+          : launch_ln_bwd<T, __nv_bfloat16>(dY, X, g, mean, rstd, M, d, dX, part, grid, st))
+  LORA_LN_DISPATCH(group, LORA_CALL)
+#undef LORA_CALL
+  if (part == nullptr) return LORA_OK;
+  launch_k(layernorm_reduce_kernel, dim3(static_cast<unsigned>(ceil_div(d, 32)), 2), dim3(256), 0, st, false,
+           static_cast<const float*>(part), grid, static_cast<int>(d), dg, db);
+  return check_launch("layernorm_reduce_kernel");
+}
+
+lora_status_t lora_linear_rotary_tables(const lora_rotary_table_desc* desc, float* cos, float* sin, void* stream) {
+  LORA_TRY(check_rotary_table(desc));
+  if (desc->n_pos > 0 && (cos == nullptr || sin == nullptr)) return LORA_ERR_INVALID_ARG;
+  if (!aligned16(cos) || !aligned16(sin)) return LORA_ERR_ALIGNMENT;
+  DevInfo dev;
+  LORA_TRY(check_arch(&dev));
+  if (desc->n_pos == 0) return LORA_OK;
+  RotaryTurns turns = {};
+  rotary_turns(desc, &turns);
+  const int pairs = desc->rot / 2;
+  const int64_t rows = 256 / (pairs / 4);
+  const int64_t blocks = ceil_div(desc->n_pos, rows), cap = static_cast<int64_t>(dev.sms) * 8;
+  launch_k(rotary_tables_kernel, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)), dim3(256), 0,
+           static_cast<cudaStream_t>(stream), false, turns, pairs, static_cast<long long>(desc->n_pos),
+           static_cast<float>(desc->amplitude), cos, sin);
+  return check_launch("rotary_tables_kernel");
+}
+
+lora_status_t lora_linear_rotary(const lora_rotary_desc* d, const lora_rope_desc* rope, const void* Q, const void* K,
+                                 void* Yq, void* Yk, void* workspace, size_t workspace_bytes, void* stream) {
+  if (d == nullptr || rope == nullptr || d->M < 0 || d->heads < 1 || d->kv_heads < 0 ||
+      (d->interleaved != 0 && d->interleaved != 1) || (d->inverse != 0 && d->inverse != 1))
+    return LORA_ERR_INVALID_ARG;
+  if (d->head_dim < 16 || d->head_dim > 2 * kRotaryMaxPairs || d->head_dim % 8 != 0 || d->rot < 16 ||
+      d->rot > d->head_dim || d->rot % 16 != 0 || d->heads > 4096 || d->kv_heads > 4096 ||
+      d->M > (int64_t(1) << 31) - 1)
+    return LORA_ERR_UNSUPPORTED;
+  if (rope->n_pos < 1 || rope->n_pos > (int64_t(1) << 31)) return LORA_ERR_INVALID_ARG;
+  if (d->M > 0 && (rope->pos == nullptr || rope->cos == nullptr || rope->sin == nullptr || Q == nullptr ||
+                   Yq == nullptr || (d->kv_heads > 0 && (K == nullptr || Yk == nullptr))))
+    return LORA_ERR_INVALID_ARG;
+  if (!aligned16(rope->cos) || !aligned16(rope->sin) || !aligned4(rope->pos) || !aligned16(Q) || !aligned16(K) ||
+      !aligned16(Yq) || !aligned16(Yk))
+    return LORA_ERR_ALIGNMENT;
+  const bool in_place = Yq == Q;
+  if (d->M > 0 && d->kv_heads > 0 && (Yk == K) != in_place) return LORA_ERR_INVALID_ARG;
+  if (workspace == nullptr || workspace_bytes < kHeaderBytes || !aligned16(workspace)) return LORA_ERR_WORKSPACE;
+  DevInfo dev;
+  LORA_TRY(check_arch(&dev));
+  if (d->M == 0) return LORA_OK;
+  RotaryParams p = {};
+  p.in[0] = static_cast<const __nv_bfloat16*>(Q);
+  p.in[1] = static_cast<const __nv_bfloat16*>(K);
+  p.out[0] = static_cast<__nv_bfloat16*>(Yq);
+  p.out[1] = static_cast<__nv_bfloat16*>(Yk);
+  p.t.pos = rope->pos;
+  p.t.cos = rope->cos;
+  p.t.sin = rope->sin;
+  p.t.n_pos = rope->n_pos;
+  p.t.half = d->rot / 2;
+  p.M = d->M;
+  p.heads[0] = d->heads;
+  p.heads[1] = d->kv_heads;
+  p.head_dim = d->head_dim;
+  p.units = d->rot / 16 + (in_place ? 0 : (d->head_dim - d->rot) / 8);
+  p.slots = static_cast<int>(ceil_div(d->heads + d->kv_heads, kRotaryHeads));
+  p.interleaved = d->interleaved;
+  p.sign = d->inverse ? -1.0f : 1.0f;
+  p.status = static_cast<uint32_t*>(workspace);
+  const int64_t blocks = ceil_div(d->M * p.units * p.slots, 256);
+  if (blocks > (int64_t(1) << 31) - 1) return LORA_ERR_UNSUPPORTED;
+  launch_k(rotary_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, static_cast<cudaStream_t>(stream), false,
+           p);
+  return check_launch("rotary_kernel");
+}
+
+size_t lora_linear_attn_plan_size(int64_t M, int64_t n_docs) {
+  return attn_plan_sizes_ok(M, n_docs) ? attn_plan_layout(M, n_docs).total : 0;
+}
+
+lora_status_t lora_linear_attn_plan(const int32_t* starts, const int32_t* prefix_len, int64_t M, int64_t n_docs,
+                                    int causal, void* plan, size_t plan_bytes, void* stream) {
+  if (M < 0 || n_docs < 0 || starts == nullptr || (causal != 0 && causal != 1)) return LORA_ERR_INVALID_ARG;
+  if (!attn_plan_sizes_ok(M, n_docs)) return LORA_ERR_UNSUPPORTED;
+  if (!aligned4(starts) || !aligned4(prefix_len)) return LORA_ERR_ALIGNMENT;
+  if (plan == nullptr || !aligned16(plan) || plan_bytes < attn_plan_layout(M, n_docs).total) return LORA_ERR_WORKSPACE;
+  DevInfo dev;
+  LORA_TRY(check_arch(&dev));
+  launch_k(attn_plan_kernel, dim3(1), dim3(1024), 0, static_cast<cudaStream_t>(stream), false, starts, prefix_len,
+           static_cast<int>(M), static_cast<int>(n_docs), causal, attn_plan_view(plan, M, n_docs));
+  return check_launch("attn_plan_kernel");
+}
+
+lora_status_t lora_linear_attn_fwd(const lora_attn_desc* d, void* plan, size_t plan_bytes, const void* Q,
+                                   const void* K, const void* V, const float* slopes, void* O, float* lse,
+                                   void* stream) {
+  LORA_TRY(check_attn_desc(d));
+  if (d->M > 0 && (Q == nullptr || K == nullptr || V == nullptr || O == nullptr || lse == nullptr))
+    return LORA_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || !aligned4(lse) || !aligned4(slopes))
+    return LORA_ERR_ALIGNMENT;
+  LORA_TRY(check_attn_plan(d, plan, plan_bytes));
+  DevInfo dev;
+  LORA_TRY(check_arch(&dev));
+  if (d->M == 0) return LORA_OK;
+  AttnParams p = attn_params(d, plan, Q, K, V, slopes, lse);
+  p.O = static_cast<__nv_bfloat16*>(O);
+  const dim3 grid(static_cast<unsigned>(p.plan.max_q), static_cast<unsigned>(d->heads));
+  launch_k(d->head_dim == 64 ? attn_rows_kernel<64, 0> : attn_rows_kernel<128, 0>, grid, dim3(128), 0,
+           static_cast<cudaStream_t>(stream), false, p);
+  return check_launch("attn_rows_kernel");
+}
+
+size_t lora_linear_attn_workspace_size(const lora_attn_desc* d) {
+  if (check_attn_desc(d) != LORA_OK) return 0;
+  return kHeaderBytes + align_up(static_cast<size_t>(d->M) * d->heads * sizeof(float), 256);
+}
+
+lora_status_t lora_linear_attn_bwd(const lora_attn_desc* d, void* plan, size_t plan_bytes, const void* dO,
+                                   const void* Q, const void* K, const void* V, const void* O, const float* lse,
+                                   const float* slopes, void* dQ, void* dK, void* dV, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  LORA_TRY(check_attn_desc(d));
+  if (d->M > 0 && (dO == nullptr || Q == nullptr || K == nullptr || V == nullptr || O == nullptr || lse == nullptr ||
+                   dQ == nullptr || dK == nullptr || dV == nullptr))
+    return LORA_ERR_INVALID_ARG;
+  if (!aligned16(dO) || !aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || !aligned16(dQ) ||
+      !aligned16(dK) || !aligned16(dV) || !aligned4(lse) || !aligned4(slopes))
+    return LORA_ERR_ALIGNMENT;
+  LORA_TRY(check_attn_plan(d, plan, plan_bytes));
+  if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < lora_linear_attn_workspace_size(d))
+    return LORA_ERR_WORKSPACE;
+  DevInfo dev;
+  LORA_TRY(check_arch(&dev));
+  if (d->M == 0) return LORA_OK;
+  AttnParams p = attn_params(d, plan, Q, K, V, slopes, const_cast<float*>(lse));
+  p.dO = static_cast<const __nv_bfloat16*>(dO);
+  p.O = static_cast<__nv_bfloat16*>(const_cast<void*>(O));
+  p.dQ = static_cast<__nv_bfloat16*>(dQ);
+  p.dK = static_cast<__nv_bfloat16*>(dK);
+  p.dV = static_cast<__nv_bfloat16*>(dV);
+  p.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  launch_k(d->head_dim == 64 ? attn_rows_kernel<64, 1> : attn_rows_kernel<128, 1>,
+           dim3(static_cast<unsigned>(p.plan.max_q), static_cast<unsigned>(d->heads)), dim3(128), 0, st, false, p);
+  LORA_TRY(check_launch("attn_rows_kernel"));
+  launch_k(d->head_dim == 64 ? attn_keys_kernel<64> : attn_keys_kernel<128>,
+           dim3(static_cast<unsigned>(p.plan.max_q), static_cast<unsigned>(d->kv_heads)), dim3(128), 0, st, false, p);
+  return check_launch("attn_keys_kernel");
 }
 
 }  // extern "C"
