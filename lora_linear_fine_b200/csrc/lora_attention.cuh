@@ -161,6 +161,115 @@ __device__ __forceinline__ bool attn_plan_ok(const AttnParams& p) {
   return false;
 }
 
+// Key tiles that the `rows` rows from row0 on see.
+__device__ __forceinline__ int attn_key_tiles(const AttnTileRef& t, int row0, int rows) {
+  const int see = max(min(row0 + rows, t.end), t.prefix_end);
+  return (see - t.begin + kAttnTile - 1) / kAttnTile;
+}
+
+// 2^x, the hardware's approximation (relative error below 2^-22).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 1 / x, the hardware's approximation (within 1 unit in the last place; 1 / inf = 0).
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Scores in the exponent of 2.  Without cap and bias the raw products stay as
+// they are and `mul` = scale log2(e) is folded into the exponent; with either
+// the values become z log2(e) and mul is 1.
+//   tanh(y) = 1 - 2 / (1 + exp(2 y)): right at both ends (0 and infinity in
+//   the denominator), absolute error a few 2^-24, so cap tanh is off by less
+//   than cap 2^-21 in the exponent.
+template <bool kCap, bool kBias>
+struct AttnScore {
+  float mul;        // of a value in the exponent of 2
+  float headroom;   // 8 / mul: how far scores may outgrow the running maximum
+  float pre, cap2, slope2;
+  __device__ __forceinline__ AttnScore(const AttnParams& p, int h) {
+    constexpr bool plain = !kCap && !kBias;
+    mul = plain ? p.scale * kLog2e : 1.0f;
+    headroom = 8.0f / mul;
+    pre = kCap ? 2.0f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
+    cap2 = kCap ? p.cap * kLog2e : 0.0f;
+    slope2 = kBias ? p.slopes[h] * kLog2e : 0.0f;
+  }
+  __device__ __forceinline__ float tanh_of(float s) const {
+    return fmaf(-2.0f, rcp_approx(1.0f + ex2(s * pre)), 1.0f);
+  }
+  // z log2(e) of one product; dist = i - j.  *t: the tanh (with a cap)
+  __device__ __forceinline__ float one(float s, float dist, float* t) const {
+    float z = s;
+    if constexpr (kCap) { *t = tanh_of(s); z = cap2 * *t; }
+    else if constexpr (kBias) z = s * pre;
+    if constexpr (kBias) z = fmaf(-slope2, fabsf(dist), z);
+    return z;
+  }
+  // a row's 128 products; dist0 = i - j of the first
+  __device__ __forceinline__ void apply(uint32_t (&v)[4][32], int dist0) const {
+    if constexpr (kCap || kBias) {
+      const float d0 = static_cast<float>(dist0);
+      float t;
+#pragma unroll
+      for (int c = 0; c < 128; ++c)
+        v[c / 32][c % 32] = __float_as_uint(one(__uint_as_float(v[c / 32][c % 32]), d0 - static_cast<float>(c), &t));
+    }
+  }
+};
+
+// Zeroes rows [first, kAttnTile) of a tile of kBoxes 128-byte column boxes in
+// shared memory and makes that visible to the tensor core.  One warp.
+template <int kBoxes>
+__device__ __forceinline__ void attn_trim_tile(uint8_t* tile, int first, int lane) {
+  for (int b = 0; b < kBoxes; ++b) {
+    uint4* rows = reinterpret_cast<uint4*>(tile + b * (kAttnTile * 128));
+    for (int i = first * 8 + lane; i < kAttnTile * 8; i += 32) rows[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// Waits for the last fill of every ring stage that has one (the aborting
+// producer's copies in flight); rp: the stage it would fill next.
+__device__ __forceinline__ void attn_drain(uint64_t* full, int stages, RingPos rp) {
+  volatile uint32_t never = 0u;
+  const AbortCtl quiet{&never, nullptr};
+  for (int i = 0; i < stages; ++i) {
+    if (i < static_cast<int>(rp.stage)) mbar_wait(&full[i], rp.phase, quiet);
+    else if (rp.phase != 0u) mbar_wait(&full[i], rp.phase ^ 1u, quiet);
+  }
+}
+
+// Rows [first, last) of one head's columns of out [M x heads * D] become zero.  Whole CTA.
+template <int D>
+__device__ __forceinline__ void attn_zero_rows(__nv_bfloat16* out, int heads, int h, int first, int last) {
+  const int n = (last - first) * (D / 8);
+  for (int i = threadIdx.x; i < n; i += blockDim.x)
+    reinterpret_cast<uint4*>(out + (static_cast<size_t>(first + i / (D / 8)) * heads + h) * D)[i % (D / 8)] =
+        make_uint4(0u, 0u, 0u, 0u);
+}
+
+// 32 fp32 values times `by` as bf16.
+__device__ __forceinline__ void attn_store32(__nv_bfloat16* out, const uint32_t (&v)[32], float by) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 8) {
+    uint4 w;
+    w.x = pack_bf16x2(__uint_as_float(v[e]) * by, __uint_as_float(v[e + 1]) * by);
+    w.y = pack_bf16x2(__uint_as_float(v[e + 2]) * by, __uint_as_float(v[e + 3]) * by);
+    w.z = pack_bf16x2(__uint_as_float(v[e + 4]) * by, __uint_as_float(v[e + 5]) * by);
+    w.w = pack_bf16x2(__uint_as_float(v[e + 6]) * by, __uint_as_float(v[e + 7]) * by);
+    *reinterpret_cast<uint4*>(out + e) = w;
+  }
+}
+
 // One warp a row and head, the head's features spread over the lanes.
 template <int D>
 struct AttnRow {

@@ -27,6 +27,7 @@
 #include "lora_layernorm.cuh"
 #include "lora_rotary.cuh"
 #include "lora_attention.cuh"
+#include "lora_attention_fwd.cuh"
 
 namespace {
 
@@ -2253,6 +2254,42 @@ AttnParams attn_params(const lora_attn_desc* d, void* plan, const void* Q, const
   return p;
 }
 
+// Tensor map of one head-interleaved operand [M x heads * D]: tiles of kAttnTile rows x 64 features.
+bool attn_tm(CUtensorMap* tm, const void* ptr, const AttnParams& p, int heads, int D) {
+  const uint64_t cols = static_cast<uint64_t>(heads) * D;
+  return make_tm(tm, ptr, cols, static_cast<uint64_t>(p.M), cols, 64, kAttnTile);
+}
+
+// Whether a kernel's registers at launch cover the shares that its warpgroups take over.
+template <typename K>
+bool regs_cover(K k, int threads, int need) {
+  cudaFuncAttributes a;
+  return cudaFuncGetAttributes(&a, k) == cudaSuccess && a.numRegs * threads >= need;
+}
+
+template <int D, bool kCap, bool kBias>
+lora_status_t launch_attn_fwd(const AttnParams& p, cudaStream_t st) {
+  AttnFwdMaps maps;
+  if (!attn_tm(&maps.q, p.Q, p, p.heads, D) || !attn_tm(&maps.k, p.K, p, p.kv_heads, D) ||
+      !attn_tm(&maps.v, p.V, p, p.kv_heads, D))
+    return LORA_ERR_CUDA;
+  auto k = attn_fwd_kernel<D, kCap, kBias>;
+  if (!regs_cover(k, kAttnFwdThreads, 128 * (kAttnFwdRegsLow + 2 * kAttnFwdRegsHigh)) ||
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnFwdCfg<D>::kSmemBytes) != cudaSuccess)
+    return cuda_error("cudaFuncSetAttribute(attn_fwd)");
+  const int64_t ctas = static_cast<int64_t>(p.plan.max_fwd) * p.heads;
+  if (ctas > (int64_t(1) << 31) - 1) return LORA_ERR_UNSUPPORTED;
+  launch_k(k, dim3(static_cast<unsigned>(ctas)), dim3(kAttnFwdThreads), AttnFwdCfg<D>::kSmemBytes, st, false, p, maps);
+  return check_launch("attn_fwd_kernel");
+}
+
+template <int D>
+lora_status_t launch_attn_fwd_mod(const AttnParams& p, cudaStream_t st) {
+  if (p.cap > 0.0f)
+    return p.slopes != nullptr ? launch_attn_fwd<D, true, true>(p, st) : launch_attn_fwd<D, true, false>(p, st);
+  return p.slopes != nullptr ? launch_attn_fwd<D, false, true>(p, st) : launch_attn_fwd<D, false, false>(p, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -2411,10 +2448,8 @@ lora_status_t lora_linear_attn_fwd(const lora_attn_desc* d, void* plan, size_t p
   if (d->M == 0) return LORA_OK;
   AttnParams p = attn_params(d, plan, Q, K, V, slopes, lse);
   p.O = static_cast<__nv_bfloat16*>(O);
-  const dim3 grid(static_cast<unsigned>(p.plan.max_q), static_cast<unsigned>(d->heads));
-  launch_k(d->head_dim == 64 ? attn_rows_kernel<64, 0> : attn_rows_kernel<128, 0>, grid, dim3(128), 0,
-           static_cast<cudaStream_t>(stream), false, p);
-  return check_launch("attn_rows_kernel");
+  return d->head_dim == 64 ? launch_attn_fwd_mod<64>(p, static_cast<cudaStream_t>(stream))
+                           : launch_attn_fwd_mod<128>(p, static_cast<cudaStream_t>(stream));
 }
 
 size_t lora_linear_attn_workspace_size(const lora_attn_desc* d) {
