@@ -149,7 +149,8 @@ struct AttnParams {
   const __nv_bfloat16 *Q, *K, *V, *dO;
   const float* slopes;           // [heads] or null
   __nv_bfloat16 *O, *dQ, *dK, *dV;
-  float *lse, *delta;            // [M x heads]
+  float* lse;                    // [M x heads]
+  float* stat;                   // backward: [2][heads][M], lse log2(e) and delta
   int M, n_docs, heads, kv_heads;
   float scale, cap;              // cap 0: none
 };
@@ -267,138 +268,6 @@ __device__ __forceinline__ void attn_store32(__nv_bfloat16* out, const uint32_t 
     w.z = pack_bf16x2(__uint_as_float(v[e + 4]) * by, __uint_as_float(v[e + 5]) * by);
     w.w = pack_bf16x2(__uint_as_float(v[e + 6]) * by, __uint_as_float(v[e + 7]) * by);
     *reinterpret_cast<uint4*>(out + e) = w;
-  }
-}
-
-// One warp a row and head, the head's features spread over the lanes.
-template <int D>
-struct AttnRow {
-  static constexpr int n = D / 32;
-  float v[n];
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-#pragma unroll
-    for (int i = 0; i < n; ++i) v[i] = __bfloat162float(p[(threadIdx.x & 31) + 32 * i]);
-  }
-  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
-#pragma unroll
-    for (int i = 0; i < n; ++i) p[(threadIdx.x & 31) + 32 * i] = __float2bfloat16_rn(v[i]);
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < n; ++i) v[i] = 0.0f;
-  }
-  __device__ __forceinline__ float dot(const AttnRow& o) const {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < n; ++i) s = fmaf(v[i], o.v[i], s);
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    return s;
-  }
-  __device__ __forceinline__ void add(float a, const AttnRow& o) {
-#pragma unroll
-    for (int i = 0; i < n; ++i) v[i] = fmaf(a, o.v[i], v[i]);
-  }
-};
-
-// z, and d z / d (scale q.k) in *slope_z.
-__device__ __forceinline__ float attn_score(const AttnParams& p, float qk, int h, int i, int j, float* dz) {
-  float z = qk * p.scale;
-  *dz = 1.0f;
-  if (p.cap > 0.0f) {
-    const float t = tanhf(z / p.cap);
-    z = p.cap * t;
-    *dz = 1.0f - t * t;
-  }
-  if (p.slopes != nullptr) z -= p.slopes[h] * fabsf(static_cast<float>(i - j));
-  return z;
-}
-
-// kind 0: o, lse; 1: delta and dq.  grid: tile x heads, 4 warps.
-template <int D, int kind>
-__global__ void __launch_bounds__(128) attn_rows_kernel(const __grid_constant__ AttnParams p) {
-  grid_dep_wait();
-  if (!attn_plan_ok(p) || blockIdx.x >= p.plan.head[kPlanQ]) return;
-  const AttnTileRef t = p.plan.q[blockIdx.x];
-  const int h = blockIdx.y, hk = h / (p.heads / p.kv_heads), lane = threadIdx.x & 31;
-  const size_t qs = static_cast<size_t>(p.heads) * D, ks = static_cast<size_t>(p.kv_heads) * D;
-  const int last = t.row0 + kAttnTile < t.end ? t.row0 + kAttnTile : t.end;
-  for (int i = t.row0 + (threadIdx.x >> 5); i < last; i += 4) {
-    const size_t at = i * qs + static_cast<size_t>(h) * D, st = static_cast<size_t>(i) * p.heads + h;
-    AttnRow<D> q, o, k, v, g;
-    o.zero();
-    const bool behind = t.prefix_end < 0;
-    const int hi = behind ? t.begin : (i + 1 > t.prefix_end ? i + 1 : t.prefix_end);
-    float m = -INFINITY, l = 0.0f, dz;
-    if (!behind) q.load(p.Q + at);
-    if constexpr (kind == 0) {
-      for (int j = t.begin; j < hi; ++j) {
-        k.load(p.K + j * ks + static_cast<size_t>(hk) * D);
-        v.load(p.V + j * ks + static_cast<size_t>(hk) * D);
-        const float z = attn_score(p, q.dot(k), h, i, j, &dz);
-        const float mn = fmaxf(m, z), a = expf(m - mn), e = expf(z - mn);
-        l = l * a + e;
-#pragma unroll
-        for (int c = 0; c < o.n; ++c) o.v[c] *= a;
-        o.add(e, v);
-        m = mn;
-      }
-      if (l > 0.0f)
-#pragma unroll
-        for (int c = 0; c < o.n; ++c) o.v[c] /= l;
-      o.store(p.O + at);
-      if (lane == 0) p.lse[st] = behind ? -INFINITY : m + logf(l);
-    } else {
-      float delta = 0.0f;
-      if (!behind) {
-        g.load(p.dO + at);
-        k.load(p.O + at);
-        delta = g.dot(k);
-      }
-      for (int j = t.begin; j < hi; ++j) {
-        k.load(p.K + j * ks + static_cast<size_t>(hk) * D);
-        v.load(p.V + j * ks + static_cast<size_t>(hk) * D);
-        const float z = attn_score(p, q.dot(k), h, i, j, &dz);
-        const float e = expf(z - p.lse[st]);
-        o.add(p.scale * e * (g.dot(v) - delta) * dz, k);
-      }
-      o.store(p.dQ + at);
-      if (lane == 0) p.delta[st] = delta;
-    }
-  }
-}
-
-// dk, dv.  grid: tile x kv heads, 4 warps.
-template <int D>
-__global__ void __launch_bounds__(128) attn_keys_kernel(const __grid_constant__ AttnParams p) {
-  grid_dep_wait();
-  if (!attn_plan_ok(p) || blockIdx.x >= p.plan.head[kPlanKv]) return;
-  const AttnTileRef t = p.plan.kv[blockIdx.x];
-  const int hk = blockIdx.y, n = p.heads / p.kv_heads;
-  const size_t qs = static_cast<size_t>(p.heads) * D, ks = static_cast<size_t>(p.kv_heads) * D;
-  const int last = t.row0 + kAttnTile < t.end ? t.row0 + kAttnTile : t.end;
-  for (int j = t.row0 + (threadIdx.x >> 5); j < last; j += 4) {
-    const size_t at = j * ks + static_cast<size_t>(hk) * D;
-    AttnRow<D> q, g, k, v, dk, dv;
-    dk.zero();
-    dv.zero();
-    if (t.prefix_end >= 0) {
-      k.load(p.K + at);
-      v.load(p.V + at);
-      for (int h = hk * n; h < (hk + 1) * n; ++h)
-        for (int i = j < t.prefix_end ? t.begin : j; i < t.end; ++i) {
-          q.load(p.Q + i * qs + static_cast<size_t>(h) * D);
-          g.load(p.dO + i * qs + static_cast<size_t>(h) * D);
-          const size_t st = static_cast<size_t>(i) * p.heads + h;
-          float dz;
-          const float z = attn_score(p, q.dot(k), h, i, j, &dz);
-          const float e = expf(z - p.lse[st]);
-          dv.add(e, g);
-          dk.add(p.scale * e * (g.dot(v) - p.delta[st]) * dz, q);
-        }
-    }
-    dk.store(p.dK + at);
-    dv.store(p.dV + at);
   }
 }
 

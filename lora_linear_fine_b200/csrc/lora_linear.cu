@@ -28,6 +28,7 @@
 #include "lora_rotary.cuh"
 #include "lora_attention.cuh"
 #include "lora_attention_fwd.cuh"
+#include "lora_attention_bwd.cuh"
 
 namespace {
 
@@ -2290,6 +2291,38 @@ lora_status_t launch_attn_fwd_mod(const AttnParams& p, cudaStream_t st) {
   return p.slopes != nullptr ? launch_attn_fwd<D, false, true>(p, st) : launch_attn_fwd<D, false, false>(p, st);
 }
 
+template <int D, bool kCap, bool kBias>
+lora_status_t launch_attn_bwd(const AttnParams& p, cudaStream_t st) {
+  AttnBwdMaps maps;
+  if (!attn_tm(&maps.q, p.Q, p, p.heads, D) || !attn_tm(&maps.k, p.K, p, p.kv_heads, D) ||
+      !attn_tm(&maps.v, p.V, p, p.kv_heads, D) || !attn_tm(&maps.d_o, p.dO, p, p.heads, D))
+    return LORA_ERR_CUDA;
+  auto kv = attn_dkv_kernel<D, kCap, kBias>;
+  auto q = attn_dq_kernel<D, kCap, kBias>;
+  constexpr int kRegs = 128 * (kAttnBwdRegsLow + 2 * kAttnBwdRegsHigh);
+  if (!regs_cover(kv, kAttnBwdThreads, kRegs) || !regs_cover(q, kAttnBwdThreads, kRegs) ||
+      cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnDkvCfg<D>::kSmemBytes) != cudaSuccess ||
+      cudaFuncSetAttribute(q, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnDqCfg<D>::kSmemBytes) != cudaSuccess)
+    return cuda_error("cudaFuncSetAttribute(attn_bwd)");
+  const int64_t ctas = static_cast<int64_t>(p.plan.max_q) * p.heads;
+  if (ctas > (int64_t(1) << 31) - 1) return LORA_ERR_UNSUPPORTED;
+  launch_k(attn_delta_kernel<D>, dim3(static_cast<unsigned>(ceil_div(p.M, 32)), static_cast<unsigned>(ceil_div(p.heads, 8))),
+           dim3(256), 0, st, false, p);
+  LORA_TRY(check_launch("attn_delta_kernel"));
+  launch_k(kv, dim3(static_cast<unsigned>(static_cast<int64_t>(p.plan.max_q) * p.kv_heads)), dim3(kAttnBwdThreads),
+           AttnDkvCfg<D>::kSmemBytes, st, false, p, maps);
+  LORA_TRY(check_launch("attn_dkv_kernel"));
+  launch_k(q, dim3(static_cast<unsigned>(ctas)), dim3(kAttnBwdThreads), AttnDqCfg<D>::kSmemBytes, st, false, p, maps);
+  return check_launch("attn_dq_kernel");
+}
+
+template <int D>
+lora_status_t launch_attn_bwd_mod(const AttnParams& p, cudaStream_t st) {
+  if (p.cap > 0.0f)
+    return p.slopes != nullptr ? launch_attn_bwd<D, true, true>(p, st) : launch_attn_bwd<D, true, false>(p, st);
+  return p.slopes != nullptr ? launch_attn_bwd<D, false, true>(p, st) : launch_attn_bwd<D, false, false>(p, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -2454,7 +2487,7 @@ lora_status_t lora_linear_attn_fwd(const lora_attn_desc* d, void* plan, size_t p
 
 size_t lora_linear_attn_workspace_size(const lora_attn_desc* d) {
   if (check_attn_desc(d) != LORA_OK) return 0;
-  return kHeaderBytes + align_up(static_cast<size_t>(d->M) * d->heads * sizeof(float), 256);
+  return kHeaderBytes + align_up(static_cast<size_t>(d->M) * d->heads * 2 * sizeof(float), 256);
 }
 
 lora_status_t lora_linear_attn_bwd(const lora_attn_desc* d, void* plan, size_t plan_bytes, const void* dO,
@@ -2480,14 +2513,9 @@ lora_status_t lora_linear_attn_bwd(const lora_attn_desc* d, void* plan, size_t p
   p.dQ = static_cast<__nv_bfloat16*>(dQ);
   p.dK = static_cast<__nv_bfloat16*>(dK);
   p.dV = static_cast<__nv_bfloat16*>(dV);
-  p.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  launch_k(d->head_dim == 64 ? attn_rows_kernel<64, 1> : attn_rows_kernel<128, 1>,
-           dim3(static_cast<unsigned>(p.plan.max_q), static_cast<unsigned>(d->heads)), dim3(128), 0, st, false, p);
-  LORA_TRY(check_launch("attn_rows_kernel"));
-  launch_k(d->head_dim == 64 ? attn_keys_kernel<64> : attn_keys_kernel<128>,
-           dim3(static_cast<unsigned>(p.plan.max_q), static_cast<unsigned>(d->kv_heads)), dim3(128), 0, st, false, p);
-  return check_launch("attn_keys_kernel");
+  p.stat = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
+  return d->head_dim == 64 ? launch_attn_bwd_mod<64>(p, static_cast<cudaStream_t>(stream))
+                           : launch_attn_bwd_mod<128>(p, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
