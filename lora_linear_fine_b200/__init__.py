@@ -641,21 +641,25 @@ def lora_linear_attn_bwd(desc, plan, plan_bytes, dO, Q, K, V, O, lse, slopes, dQ
                                          workspace, workspace_bytes, stream))
 
 
-def _need(ok, what):
-    if not ok:
-        raise LoraError(1, what)
+def _refuse(what):
+    raise LoraError(1, what)
 
 
-def _tensors(device, named):
-    """Checks {name: (tensor or None, dtype, shape)}: device, type, shape, density.  A dimension of None is any."""
-    for name, (t, dtype, shape) in named.items():
+def _tensors(device, *named):
+    """Checks (name, tensor or None, dtype, shape): device, type, shape, density.  A dimension of None is any."""
+    for name, t, dtype, shape in named:
         if t is None:
             continue
-        _need(t.device == device, f"{name} is on {t.device}, not {device}")
-        _need(t.dtype == dtype, f"{name} is {t.dtype}, not {dtype}")
-        _need(t.dim() == len(shape) and all(w is None or n == w for n, w in zip(t.shape, shape)),
-              f"{name} has shape {tuple(t.shape)}, not {shape}")
-        _need(t.is_contiguous(), f"{name} is not contiguous")
+        if t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous():
+            continue
+        if t.device != device:
+            _refuse(f"{name} is on {t.device}, not {device}")
+        if t.dtype != dtype:
+            _refuse(f"{name} is {t.dtype}, not {dtype}")
+        if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+            _refuse(f"{name} has shape {tuple(t.shape)}, not {shape}")
+        if not t.is_contiguous():
+            _refuse(f"{name} is not contiguous")
 
 
 class _On:
@@ -663,28 +667,37 @@ class _On:
     current stream) as the current ones, so that outputs belong to the stream
     that writes them; the inputs are recorded on a stream of the caller's."""
 
+    __slots__ = ("_ctx", "_handle")
+
     def __init__(self, device, stream, *inputs):
         import torch
-        _need(device.type == "cuda", f"the tensors are on {device}, not on a CUDA device")
-        if stream is not None:
-            _need(stream.device == device, f"the stream is on {stream.device}, not {device}")
-            for t in inputs:
-                if t is not None:
-                    t.record_stream(stream)
-        self._ctx = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
+        if device.type != "cuda":
+            _refuse(f"the tensors are on {device}, not on a CUDA device")
+        if stream is None:
+            self._ctx = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+            self._handle = torch._C._cuda_getCurrentRawStream(device.index)
+            return
+        if stream.device != device:
+            _refuse(f"the stream is on {stream.device}, not {device}")
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
+        self._ctx, self._handle = torch.cuda.stream(stream), stream.cuda_stream
 
     def __enter__(self):
-        self._ctx.__enter__()
-        return _stream_handle()
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return self._handle
 
     def __exit__(self, *exc):
-        return self._ctx.__exit__(*exc)
+        return None if self._ctx is None else self._ctx.__exit__(*exc)
 
 
 def _workspace(workspace, nbytes, device):
     if workspace is None:
         return Workspace(nbytes, device)
-    _need(workspace.buf.device == device, f"the workspace is on {workspace.buf.device}, not {device}")
+    if workspace.buf.device != device:
+        _refuse(f"the workspace is on {workspace.buf.device}, not {device}")
     return workspace.ensure(nbytes)
 
 
@@ -693,10 +706,11 @@ def layer_norm(X, g, b=None, eps=1e-5, stream=None):
     scale g and shift b (bf16 [d]; b may be None); mean, rstd fp32 [M] are the
     backward's inputs."""
     import torch
-    _need(X.dim() == 2, f"X has shape {tuple(X.shape)}")
+    if X.dim() != 2:
+        _refuse(f"X has shape {tuple(X.shape)}")
     M, d = X.shape
     bf16, f32 = torch.bfloat16, torch.float32
-    _tensors(X.device, {"X": (X, bf16, (M, d)), "g": (g, bf16, (d,)), "b": (b, bf16, (d,))})
+    _tensors(X.device, ("X", X, bf16, (M, d)), ("g", g, bf16, (d,)), ("b", b, bf16, (d,)))
     with _On(X.device, stream, X, g, b) as st:
         Y = torch.empty_like(X)
         mean, rstd = (torch.empty(M, dtype=f32, device=X.device) for _ in range(2))
@@ -709,12 +723,14 @@ def layer_norm_backward(dY, X, g, mean, rstd, bias=True, workspace=None, stream=
     """(dX, dg, db) for dY bf16 or fp32 [M x d]; dg, db fp32 [d] (db None
     without ``bias``)."""
     import torch
-    _need(X.dim() == 2, f"X has shape {tuple(X.shape)}")
+    if X.dim() != 2:
+        _refuse(f"X has shape {tuple(X.shape)}")
     M, d = X.shape
     bf16, f32 = torch.bfloat16, torch.float32
-    _need(dY.dtype in (bf16, f32), f"dY is {dY.dtype}, not bfloat16 or float32")
-    _tensors(X.device, {"dY": (dY, dY.dtype, (M, d)), "X": (X, bf16, (M, d)), "g": (g, bf16, (d,)),
-                        "mean": (mean, f32, (M,)), "rstd": (rstd, f32, (M,))})
+    if dY.dtype not in (bf16, f32):
+        _refuse(f"dY is {dY.dtype}, not bfloat16 or float32")
+    _tensors(X.device, ("dY", dY, dY.dtype, (M, d)), ("X", X, bf16, (M, d)), ("g", g, bf16, (d,)),
+             ("mean", mean, f32, (M,)), ("rstd", rstd, f32, (M,)))
     with _On(X.device, stream, dY, X, g, mean, rstd) as st:
         dX = torch.empty_like(X)
         dg = torch.empty(d, dtype=f32, device=X.device)
@@ -732,8 +748,10 @@ def rotary_tables(n_pos, rot, base=10000.0, scaling="none", factor=1.0, low=1.0,
     under a scaling of ROTARY_SCALINGS; low and high are numbers of turns over
     the ``original`` context ("wavelength", "ramp")."""
     import torch
-    _need(scaling in ROTARY_SCALINGS, f"scaling {scaling!r} is none of {sorted(ROTARY_SCALINGS)}")
-    _need(n_pos >= 0 and rot >= 0, f"n_pos {n_pos}, rot {rot}")
+    if scaling not in ROTARY_SCALINGS:
+        _refuse(f"scaling {scaling!r} is none of {sorted(ROTARY_SCALINGS)}")
+    if n_pos < 0 or rot < 0:
+        _refuse(f"n_pos {n_pos}, rot {rot}")
     if device is None:
         device = torch.device("cuda", torch.cuda.current_device()) if stream is None else stream.device
     device = torch.device(device)
@@ -752,14 +770,18 @@ def rotary(Q, K, pos, cos, sin, head_dim, layout="half", inverse=False, inplace=
     [n_pos x rot/2]; the first rot features of each head take part.
     ``inverse`` turns back: the gradients of Q and K from those of Yq and Yk."""
     import torch
-    _need(layout in ROTARY_LAYOUTS, f"layout {layout!r} is none of {sorted(ROTARY_LAYOUTS)}")
-    _need(Q.dim() == 2 and cos.dim() == 2, f"Q has shape {tuple(Q.shape)}, cos {tuple(cos.shape)}")
+    if layout not in ROTARY_LAYOUTS:
+        _refuse(f"layout {layout!r} is none of {sorted(ROTARY_LAYOUTS)}")
+    if Q.dim() != 2 or cos.dim() != 2:
+        _refuse(f"Q has shape {tuple(Q.shape)}, cos {tuple(cos.shape)}")
     M, n_pos, rot = Q.shape[0], cos.shape[0], 2 * cos.shape[1]
-    _need(head_dim > 0 and Q.shape[1] % head_dim == 0, f"{Q.shape[1]} features are no heads of {head_dim}")
-    _need(K is None or (K.dim() == 2 and K.shape[1] % head_dim == 0), f"K's features are no heads of {head_dim}")
+    if head_dim <= 0 or Q.shape[1] % head_dim != 0:
+        _refuse(f"{Q.shape[1]} features are no heads of {head_dim}")
+    if K is not None and (K.dim() != 2 or K.shape[1] % head_dim != 0):
+        _refuse(f"K's features are no heads of {head_dim}")
     bf16, f32 = torch.bfloat16, torch.float32
-    _tensors(Q.device, {"Q": (Q, bf16, (M, None)), "K": (K, bf16, (M, None)), "pos": (pos, torch.int32, (M,)),
-                        "cos": (cos, f32, (n_pos, rot // 2)), "sin": (sin, f32, (n_pos, rot // 2))})
+    _tensors(Q.device, ("Q", Q, bf16, Q.shape), ("K", K, bf16, (M, None if K is None else K.shape[1])),
+             ("pos", pos, torch.int32, (M,)), ("cos", cos, f32, cos.shape), ("sin", sin, f32, cos.shape))
     desc = make_rotary_desc(M, Q.shape[1] // head_dim, 0 if K is None else K.shape[1] // head_dim, head_dim, rot,
                             layout, inverse)
     rope = make_rope_desc(_ptr(pos), _ptr(cos), _ptr(sin), n_pos, head_dim)
@@ -782,11 +804,13 @@ class AttentionPlan:
 
     def __init__(self, starts, M, prefix_len=None, causal=True, stream=None):
         import torch
-        _need(starts.dim() == 1 and starts.numel() >= 1, f"starts has shape {tuple(starts.shape)}")
+        if starts.dim() != 1 or starts.numel() < 1:
+            _refuse(f"starts has shape {tuple(starts.shape)}")
         n = starts.numel() - 1
-        _tensors(starts.device, {"starts": (starts, torch.int32, (n + 1,)), "prefix_len": (prefix_len, torch.int32, (n,))})
+        _tensors(starts.device, ("starts", starts, torch.int32, (n + 1,)), ("prefix_len", prefix_len, torch.int32, (n,)))
         self.M, self.n_docs, self.causal, self.nbytes = int(M), n, bool(causal), lora_linear_attn_plan_size(M, n)
-        _need(self.nbytes > 0, f"{M} rows in {n} documents")
+        if self.nbytes <= 0:
+            _refuse(f"{M} rows in {n} documents")
         with _On(starts.device, stream, starts, prefix_len) as st:
             self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=starts.device)
             _check(lora_linear_attn_plan(_ptr(starts), _ptr(prefix_len), self.M, n, self.causal, self.buf.data_ptr(),
@@ -796,15 +820,16 @@ class AttentionPlan:
         return lora_linear_device_status(self.buf.data_ptr(), _stream_handle(stream))[1]
 
 
-def _attention_args(Q, K, V, plan, heads, kv_heads, scale, softcap, slopes, more):
+def _attention_args(Q, K, V, plan, heads, kv_heads, scale, softcap, slopes):
     import torch
-    _need(Q.dim() == 2 and heads > 0 and kv_heads > 0 and Q.shape[1] % heads == 0,
-          f"Q has shape {tuple(Q.shape)} for {heads} heads")
+    if Q.dim() != 2 or heads <= 0 or kv_heads <= 0 or Q.shape[1] % heads != 0:
+        _refuse(f"Q has shape {tuple(Q.shape)} for {heads} heads")
     M, D, bf16 = Q.shape[0], Q.shape[1] // heads, torch.bfloat16
-    _need(M == plan.M, f"{M} rows with a plan of {plan.M}")
-    _tensors(Q.device, {"Q": (Q, bf16, (M, heads * D)), "K": (K, bf16, (M, kv_heads * D)),
-                        "V": (V, bf16, (M, kv_heads * D)), "slopes": (slopes, torch.float32, (heads,)),
-                        "the plan": (plan.buf, torch.uint8, (plan.nbytes,))} | more(M, D))
+    if M != plan.M:
+        _refuse(f"{M} rows with a plan of {plan.M}")
+    _tensors(Q.device, ("Q", Q, bf16, (M, heads * D)), ("K", K, bf16, (M, kv_heads * D)),
+             ("V", V, bf16, (M, kv_heads * D)), ("slopes", slopes, torch.float32, (heads,)),
+             ("the plan", plan.buf, torch.uint8, (plan.nbytes,)))
     return make_attn_desc(M, plan.n_docs, heads, kv_heads, D, plan.causal, scale, softcap)
 
 
@@ -815,7 +840,7 @@ def attention(Q, K, V, plan, heads, kv_heads, scale=None, softcap=0.0, slopes=No
     [heads]) subtract slope * |i - j|.  lse fp32 [M x heads] is the backward's
     input."""
     import torch
-    desc = _attention_args(Q, K, V, plan, heads, kv_heads, scale, softcap, slopes, lambda M, D: {})
+    desc = _attention_args(Q, K, V, plan, heads, kv_heads, scale, softcap, slopes)
     with _On(Q.device, stream, Q, K, V, slopes, plan.buf) as st:
         O = torch.empty_like(Q)
         lse = torch.empty((Q.shape[0], heads), dtype=torch.float32, device=Q.device)
@@ -828,9 +853,9 @@ def attention_backward(dO, Q, K, V, O, lse, plan, heads, kv_heads, scale=None, s
                        workspace=None, stream=None):
     """(dQ, dK, dV) of ``attention`` for its O and lse."""
     import torch
-    desc = _attention_args(Q, K, V, plan, heads, kv_heads, scale, softcap, slopes, lambda M, D: {
-        "dO": (dO, torch.bfloat16, (M, heads * D)), "O": (O, torch.bfloat16, (M, heads * D)),
-        "lse": (lse, torch.float32, (M, heads))})
+    desc = _attention_args(Q, K, V, plan, heads, kv_heads, scale, softcap, slopes)
+    _tensors(Q.device, ("dO", dO, torch.bfloat16, Q.shape), ("O", O, torch.bfloat16, Q.shape),
+             ("lse", lse, torch.float32, (plan.M, heads)))
     with _On(Q.device, stream, dO, Q, K, V, O, lse, slopes, plan.buf) as st:
         dQ, dK, dV = torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V)
         ws = _workspace(workspace, lora_linear_attn_workspace_size(desc), Q.device)

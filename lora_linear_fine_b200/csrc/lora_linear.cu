@@ -2089,6 +2089,24 @@ lora_status_t lora_linear_ce_fwd_bwd(const lora_ce_desc* d, const void* H, const
 // ===========================================================================
 namespace {
 
+// Makes a kernel ready on the current device, once: its dynamic shared memory
+// and, where its warpgroups share out registers, that those at launch cover
+// `regs` (0: they do not).
+template <auto kKernel>
+lora_status_t kernel_ready(int smem, int threads = 0, int regs = 0) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cuda_error("cudaGetDevice");
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return LORA_OK;
+  cudaFuncAttributes a;
+  if (cudaFuncGetAttributes(&a, kKernel) != cudaSuccess || a.numRegs * threads < regs ||
+      cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return cuda_error("a kernel's attributes");
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return LORA_OK;
+}
+
 // Threads a row: the smallest group whose kLnNV chunks a thread hold d features.
 int ln_group(int64_t d) {
   int t = 32;
@@ -2101,10 +2119,6 @@ int ln_grid(int64_t M, int group, int per_sm, const DevInfo& dev) {
   const int64_t cap = static_cast<int64_t>(dev.sms) * per_sm;
   return static_cast<int>(blocks < cap ? blocks : cap);
 }
-
-// CTAs that stay for their rows in the backward: enough threads to fill the
-// SMs, and no more partial rows than that.
-constexpr int kLnBwdPerSm = 2;
 
 lora_status_t check_layernorm(const void* X, const void* g, int64_t M, int64_t d, const void* out, const float* mean,
                               const float* rstd) {
@@ -2119,21 +2133,53 @@ lora_status_t check_layernorm(const void* X, const void* g, int64_t M, int64_t d
 template <int T>
 lora_status_t launch_ln_fwd(const void* X, const void* g, const void* b, int64_t M, int64_t d, float eps, void* Y,
                             float* mean, float* rstd, const DevInfo& dev, cudaStream_t st) {
-  launch_k(layernorm_fwd_kernel<T>, dim3(ln_grid(M, T, 2048 / LnCfg<T>::kThreads, dev)), dim3(LnCfg<T>::kThreads), 0,
+  launch_k(layernorm_fwd_kernel<T>, dim3(ln_grid(M, T, LnCfg<T>::kPerSm, dev)), dim3(LnCfg<T>::kThreads), 0,
            st, false, static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(g),
            static_cast<const __nv_bfloat16*>(b), static_cast<long long>(M), static_cast<int>(d), eps,
            static_cast<__nv_bfloat16*>(Y), mean, rstd);
   return check_launch("layernorm_fwd_kernel");
 }
 
-template <int T, typename TDy>
+// A stage holds as many rows as keep it near kLnStageBytes, a multiple of the
+// CTA's groups; fewer when the rows do not go round (then latency counts).
+template <int T, int NV, typename TDy>
 lora_status_t launch_ln_bwd(const void* dY, const void* X, const void* g, const float* mean, const float* rstd,
-                            int64_t M, int64_t d, void* dX, float* part, int grid, cudaStream_t st) {
-  const size_t smem = LnCfg<T>::kGroups > 1 ? static_cast<size_t>(2 * d) * 4 : 0;
-  launch_k(layernorm_bwd_kernel<T, TDy>, dim3(grid), dim3(LnCfg<T>::kThreads), smem, st, false,
+                            int64_t M, int64_t d, void* dX, float* part, int want_db, int sms, uint32_t* status, int* grid,
+                            cudaStream_t st) {
+  constexpr int kGroups = kLnBwdThreads / T;
+  const int64_t row_bytes = d * static_cast<int64_t>(2 + sizeof(TDy));
+  int64_t rows = 2 * kGroups * std::max<int64_t>(1, kLnStageBytes / (2 * kGroups * row_bytes));
+  if (3 * rows * row_bytes > kLnRingBytes) rows = kGroups;       // no room for pairs of rows
+  rows = std::min(rows, ceil_div(M, sms));
+  LnBwdShape sh;
+  sh.rows = static_cast<int>(rows);
+  sh.stages = static_cast<int>(std::min<int64_t>(kLnMaxStages, kLnRingBytes / (rows * row_bytes)));
+  const int64_t ring = sh.stages * rows * row_bytes, acc = kGroups > 1 ? 2 * d * 4 : 0;
+  const size_t smem = static_cast<size_t>(std::max(ring + kGroups * d * 2, acc));      // g behind the ring, a copy a group
+  *grid = static_cast<int>(std::min<int64_t>(sms, ceil_div(M, rows)));
+  constexpr auto k = layernorm_bwd_kernel<T, NV, TDy>;
+  LORA_TRY(kernel_ready<k>(kLnRingBytes + kLnMaxD * 2));
+  launch_k(k, dim3(static_cast<unsigned>(*grid)), dim3(kLnBwdThreads), smem, st, false,
            static_cast<const TDy*>(dY), static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(g),
-           mean, rstd, static_cast<long long>(M), static_cast<int>(d), static_cast<__nv_bfloat16*>(dX), part);
+           mean, rstd, static_cast<long long>(M), static_cast<int>(d), static_cast<__nv_bfloat16*>(dX), part, sh,
+           want_db, status);
   return check_launch("layernorm_bwd_kernel");
+}
+
+template <typename TDy>
+lora_status_t launch_ln_bwd_d(const void* dY, const void* X, const void* g, const float* mean, const float* rstd,
+                              int64_t M, int64_t d, void* dX, float* part, int want_db, int sms, uint32_t* status, int* grid,
+                              cudaStream_t st) {
+#define LORA_CALL(T, NV) launch_ln_bwd<T, NV, TDy>(dY, X, g, mean, rstd, M, d, dX, part, want_db, sms, status, grid, st)
+  if (d > 8192) return LORA_CALL(512, 4);
+  switch (ln_group(d)) {
+    case 32: return LORA_CALL(32, 2);
+    case 64: return LORA_CALL(64, 2);
+    case 128: return LORA_CALL(128, 2);
+    case 256: return LORA_CALL(256, 2);
+    default: return LORA_CALL(512, 2);
+  }
+#undef LORA_CALL
 }
 
 #define LORA_LN_DISPATCH(group, call)      \
@@ -2261,23 +2307,14 @@ bool attn_tm(CUtensorMap* tm, const void* ptr, const AttnParams& p, int heads, i
   return make_tm(tm, ptr, cols, static_cast<uint64_t>(p.M), cols, 64, kAttnTile);
 }
 
-// Whether a kernel's registers at launch cover the shares that its warpgroups take over.
-template <typename K>
-bool regs_cover(K k, int threads, int need) {
-  cudaFuncAttributes a;
-  return cudaFuncGetAttributes(&a, k) == cudaSuccess && a.numRegs * threads >= need;
-}
-
 template <int D, bool kCap, bool kBias>
 lora_status_t launch_attn_fwd(const AttnParams& p, cudaStream_t st) {
   AttnFwdMaps maps;
   if (!attn_tm(&maps.q, p.Q, p, p.heads, D) || !attn_tm(&maps.k, p.K, p, p.kv_heads, D) ||
       !attn_tm(&maps.v, p.V, p, p.kv_heads, D))
     return LORA_ERR_CUDA;
-  auto k = attn_fwd_kernel<D, kCap, kBias>;
-  if (!regs_cover(k, kAttnFwdThreads, 128 * (kAttnFwdRegsLow + 2 * kAttnFwdRegsHigh)) ||
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnFwdCfg<D>::kSmemBytes) != cudaSuccess)
-    return cuda_error("cudaFuncSetAttribute(attn_fwd)");
+  constexpr auto k = attn_fwd_kernel<D, kCap, kBias>;
+  LORA_TRY(kernel_ready<k>(AttnFwdCfg<D>::kSmemBytes, kAttnFwdThreads, 128 * (kAttnFwdRegsLow + 2 * kAttnFwdRegsHigh)));
   const int64_t ctas = static_cast<int64_t>(p.plan.max_fwd) * p.heads;
   if (ctas > (int64_t(1) << 31) - 1) return LORA_ERR_UNSUPPORTED;
   launch_k(k, dim3(static_cast<unsigned>(ctas)), dim3(kAttnFwdThreads), AttnFwdCfg<D>::kSmemBytes, st, false, p, maps);
@@ -2297,13 +2334,11 @@ lora_status_t launch_attn_bwd(const AttnParams& p, cudaStream_t st) {
   if (!attn_tm(&maps.q, p.Q, p, p.heads, D) || !attn_tm(&maps.k, p.K, p, p.kv_heads, D) ||
       !attn_tm(&maps.v, p.V, p, p.kv_heads, D) || !attn_tm(&maps.d_o, p.dO, p, p.heads, D))
     return LORA_ERR_CUDA;
-  auto kv = attn_dkv_kernel<D, kCap, kBias>;
-  auto q = attn_dq_kernel<D, kCap, kBias>;
+  constexpr auto kv = attn_dkv_kernel<D, kCap, kBias>;
+  constexpr auto q = attn_dq_kernel<D, kCap, kBias>;
   constexpr int kRegs = 128 * (kAttnBwdRegsLow + 2 * kAttnBwdRegsHigh);
-  if (!regs_cover(kv, kAttnBwdThreads, kRegs) || !regs_cover(q, kAttnBwdThreads, kRegs) ||
-      cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnDkvCfg<D>::kSmemBytes) != cudaSuccess ||
-      cudaFuncSetAttribute(q, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnDqCfg<D>::kSmemBytes) != cudaSuccess)
-    return cuda_error("cudaFuncSetAttribute(attn_bwd)");
+  LORA_TRY(kernel_ready<kv>(AttnDkvCfg<D>::kSmemBytes, kAttnBwdThreads, kRegs));
+  LORA_TRY(kernel_ready<q>(AttnDqCfg<D>::kSmemBytes, kAttnBwdThreads, kRegs));
   const int64_t ctas = static_cast<int64_t>(p.plan.max_q) * p.heads;
   if (ctas > (int64_t(1) << 31) - 1) return LORA_ERR_UNSUPPORTED;
   launch_k(attn_delta_kernel<D>, dim3(static_cast<unsigned>(ceil_div(p.M, 32)), static_cast<unsigned>(ceil_div(p.heads, 8))),
@@ -2344,10 +2379,7 @@ lora_status_t lora_linear_layernorm_fwd(const void* X, const void* g, const void
 
 size_t lora_linear_layernorm_workspace_size(int64_t M, int64_t d) {
   if (M < 0 || M > (int64_t(1) << 40) || d <= 0 || d > kLnMaxD || d % 8 != 0) return 0;
-  const int group = ln_group(d);
-  const int64_t blocks = ceil_div(M, group >= 256 ? 1 : 256 / group);
-  const int64_t most = static_cast<int64_t>(kTargetCtas) * kLnBwdPerSm;
-  return kHeaderBytes + static_cast<size_t>(blocks < most ? blocks : most) * 2 * d * sizeof(float);
+  return kHeaderBytes + static_cast<size_t>(M < kTargetCtas ? M : kTargetCtas) * 2 * d * sizeof(float);
 }
 
 lora_status_t lora_linear_layernorm_bwd(const void* dY, int dy_f32, const void* X, const void* g, const float* mean,
@@ -2368,18 +2400,15 @@ lora_status_t lora_linear_layernorm_bwd(const void* dY, int dy_f32, const void* 
       return cuda_error("cudaMemsetAsync(db)");
     return LORA_OK;
   }
-  DevInfo grid_dev = dev;
-  if (grid_dev.sms > kTargetCtas) grid_dev.sms = kTargetCtas;    // the workspace is sized without a device
-  const int group = ln_group(d), grid = ln_grid(M, group, kLnBwdPerSm, grid_dev);
+  const int sms = dev.sms < kTargetCtas ? dev.sms : kTargetCtas;    // the workspace is sized without a device
   float* part = dg != nullptr || db != nullptr
                     ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes) : nullptr;
-#define LORA_CALL(T)                                                                                    \
-  (dy_f32 ? launch_ln_bwd<T, float>(dY, X, g, mean, rstd, M, d, dX, part, grid, st)                     \
-          : launch_ln_bwd<T, __nv_bfloat16>(dY, X, g, mean, rstd, M, d, dX, part, grid, st))
-  LORA_LN_DISPATCH(group, LORA_CALL)
-#undef LORA_CALL
+  uint32_t* status = static_cast<uint32_t*>(workspace);
+  int grid = 0;
+  LORA_TRY(dy_f32 ? launch_ln_bwd_d<float>(dY, X, g, mean, rstd, M, d, dX, part, db != nullptr, sms, status, &grid, st)
+                  : launch_ln_bwd_d<__nv_bfloat16>(dY, X, g, mean, rstd, M, d, dX, part, db != nullptr, sms, status, &grid, st));
   if (part == nullptr) return LORA_OK;
-  launch_k(layernorm_reduce_kernel, dim3(static_cast<unsigned>(ceil_div(d, 32)), 2), dim3(256), 0, st, false,
+  launch_k(layernorm_reduce_kernel, dim3(static_cast<unsigned>(ceil_div(d, 128)), db != nullptr ? 2 : 1), dim3(1024), 0, st, false,
            static_cast<const float*>(part), grid, static_cast<int>(d), dg, db);
   return check_launch("layernorm_reduce_kernel");
 }
