@@ -184,47 +184,143 @@ __device__ __forceinline__ float rcp_approx(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Scores in the exponent of 2.  Without cap and bias the raw products stay as
-// they are and `mul` = scale log2(e) is folded into the exponent; with either
-// the values become z log2(e) and mul is 1.
-//   tanh(y) = 1 - 2 / (1 + exp(2 y)): right at both ends (0 and infinity in
-//   the denominator), absolute error a few 2^-24, so cap tanh is off by less
-//   than cap 2^-21 in the exponent.
+// The larger of three values (NaN only if all are).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 pair_of(const uint32_t* v) {
+  return make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+}
+
+// 2^x of a pair on the FMA pipe: x = n + f with n whole and |f| <= 1/2 (adding
+// 1.5 * 2^23 leaves n in the low bits), 2^f by a polynomial of degree 4 with
+// the least largest relative error on that interval (2^-18.5), n added to the
+// exponent.  Below -126 the result is 2^-126.  The special function unit gives
+// 16 exponentials a cycle and SM, fewer than a tile's products leave time for;
+// so the kernels form part of them this way.
+__device__ __forceinline__ float2 exp2_poly(float2 x) {
+  constexpr float kRound = 12582912.0f;
+  x = make_float2(max_nan(x.x, -126.0f), max_nan(x.y, -126.0f));
+  const float2 t = add2(x, both(kRound));
+  const float2 f = fma2(add2(t, both(-kRound)), both(-1.0f), x);
+  float2 p = fma2(both(0.009570102207362652f), f, both(0.05591785907745361f));
+  p = fma2(p, f, both(0.240247443318367f));
+  p = fma2(p, f, both(0.6931217908859253f));
+  p = fma2(p, f, both(0.9999992847442627f));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+
+// 2^x of the i-th pair of a row: kPoly of four pairs by the polynomial.
+template <int kPoly>
+__device__ __forceinline__ float2 attn_exp2(float2 x, int i) {
+  return (i & 3) < kPoly ? exp2_poly(x) : make_float2(ex2(x.x), ex2(x.y));
+}
+
+// Scores as values whose exponent of 2 is `mul` times them: the raw products
+// (mul = scale log2(e)), with a cap the tanh (mul = cap log2(e)), with a bias
+// z log2(e) (mul = 1).
+//   tanh(y) = y P(y^2), P of degree 4 with the least largest error for
+//   |y| <= 0.6 (2^-23.7), where all of a warp's values are that small: FMAs
+//   alone.  Else tanh(y) = 1 - 2 / (1 + exp(2 y)), two special functions, right
+//   at both ends (0 and infinity in the denominator), within a few 2^-24.
 template <bool kCap, bool kBias>
 struct AttnScore {
-  float mul;        // of a value in the exponent of 2
-  float headroom;   // 8 / mul: how far scores may outgrow the running maximum
+  float mul;
+  float headroom;   // 8 / mul: how far values may outgrow the running maximum
   float pre, cap2, slope2;
   __device__ __forceinline__ AttnScore(const AttnParams& p, int h) {
-    constexpr bool plain = !kCap && !kBias;
-    mul = plain ? p.scale * kLog2e : 1.0f;
-    headroom = 8.0f / mul;
-    pre = kCap ? 2.0f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
     cap2 = kCap ? p.cap * kLog2e : 0.0f;
+    pre = kCap ? p.scale / p.cap : p.scale * kLog2e;
     slope2 = kBias ? p.slopes[h] * kLog2e : 0.0f;
+    mul = kBias ? 1.0f : kCap ? cap2 : pre;
+    headroom = 8.0f / mul;
   }
-  __device__ __forceinline__ float tanh_of(float s) const {
-    return fmaf(-2.0f, rcp_approx(1.0f + ex2(s * pre)), 1.0f);
-  }
-  // z log2(e) of one product; dist = i - j.  *t: the tanh (with a cap)
-  __device__ __forceinline__ float one(float s, float dist, float* t) const {
-    float z = s;
-    if constexpr (kCap) { *t = tanh_of(s); z = cap2 * *t; }
-    else if constexpr (kBias) z = s * pre;
-    if constexpr (kBias) z = fmaf(-slope2, fabsf(dist), z);
-    return z;
-  }
-  // a row's 128 products; dist0 = i - j of the first
-  __device__ __forceinline__ void apply(uint32_t (&v)[4][32], int dist0) const {
-    if constexpr (kCap || kBias) {
-      const float d0 = static_cast<float>(dist0);
-      float t;
+  // 32 kChunks products of a row in place; dist0 = distance (either sign) of
+  // the first, rising by 1 (kUp) or falling by 1 from one to the next.
+  // dt: 1 - tanh^2 (only with a cap).
+  template <int kChunks, bool kUp, bool kWantDt>
+  __device__ __forceinline__ void apply(uint32_t (&v)[kChunks][32], int dist0, float2* dt) const {
+    if constexpr (kCap) {
+      float top = 0.0f;
 #pragma unroll
-      for (int c = 0; c < 128; ++c)
-        v[c / 32][c % 32] = __float_as_uint(one(__uint_as_float(v[c / 32][c % 32]), d0 - static_cast<float>(c), &t));
+      for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) top = max3_abs(top, __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+      if (!__any_sync(0xffffffffu, top * pre > 0.6f)) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 y = mul2(pair_of(&v[c][e]), both(pre)), u = mul2(y, y);
+            float2 q = fma2(both(0.015504649840295315f), u, both(-0.052122555673122406f));
+            q = fma2(q, u, both(0.13310648500919342f));
+            q = fma2(q, u, both(-0.3333234488964081f));
+            q = fma2(q, u, both(0.9999999403953552f));
+            put(v[c], e, mul2(y, q));
+          }
+      } else {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            v[c][e] = __float_as_uint(
+                fmaf(-2.0f, rcp_approx(1.0f + ex2(__uint_as_float(v[c][e]) * (2.0f * kLog2e * pre))), 1.0f));
+      }
+      if constexpr (kWantDt) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 t = pair_of(&v[c][e]);
+            dt[16 * c + e / 2] = fma2(make_float2(-t.x, -t.y), t, both(1.0f));
+          }
+      }
+    }
+    if constexpr (kBias) {
+      const float2 d0 = both(static_cast<float>(dist0));
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          constexpr float kSign = kUp ? 1.0f : -1.0f;
+          const float2 d = add2(d0, make_float2(kSign * (32 * c + e), kSign * (32 * c + e + 1)));
+          const float2 z = mul2(pair_of(&v[c][e]), both(kCap ? cap2 : pre));
+          put(v[c], e, make_float2(fmaf(-slope2, fabsf(d.x), z.x), fmaf(-slope2, fabsf(d.y), z.y)));
+        }
     }
   }
+  __device__ __forceinline__ static void put(uint32_t (&v)[32], int e, float2 z) {
+    v[e] = __float_as_uint(z.x);
+    v[e + 1] = __float_as_uint(z.y);
+  }
 };
+
+// 32 registers that a tmem load fills are read after this point only.
+__device__ __forceinline__ void attn_hold(uint32_t (&v)[32]) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(v[e]));
+}
+
+// The warp's stores to tensor memory are done: tell the MMA warp.
+__device__ __forceinline__ void attn_publish(uint64_t* bar, int lane) {
+  tmem_wait_st();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
 
 // Zeroes rows [first, kAttnTile) of a tile of kBoxes 128-byte column boxes in
 // shared memory and makes that visible to the tensor core.  One warp.

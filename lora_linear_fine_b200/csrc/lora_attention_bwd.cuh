@@ -16,6 +16,7 @@
 namespace lora {
 
 constexpr int kAttnBwdThreads = 384;     // warps: TMA, MMA, statistics, trimming, two warpgroups of elementwise work
+constexpr int kAttnBwdPoly = 1;          // of four pairs of exponentials, those by the polynomial
 constexpr int kAttnBwdRegsLow = 104, kAttnBwdRegsHigh = 200;
 
 struct AttnBwdMaps {
@@ -59,24 +60,18 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
   p.stat[static_cast<size_t>(p.heads + h) * p.M + m] = s[threadIdx.x >> 5][threadIdx.x & 31];
 }
 
-// One 16-key (or 16-query) step of a product whose A operand was written to
-// tensor memory by two warpgroups, 64 columns of the tile each: the first
-// half's 32 packed columns at `base`, the second half's at base + 64.
-__device__ __forceinline__ uint32_t attn_half_step(uint32_t base, int kk) { return base + (kk / 4) * 64 + 8 * (kk % 4); }
+// The A operand of dV, dK and dQ is written to tensor memory by two
+// warpgroups, 64 columns of the tile each (the first one's 32 packed columns at
+// `base`, the second one's at base + 64), in two parts of 32.  Part c of both
+// is four steps of 16 out of the product's eight: k = 0 .. 3 -> step.
+__device__ __forceinline__ int attn_part_step(int c, int k) { return (k / 2) * 4 + 2 * c + k % 2; }
+__device__ __forceinline__ uint32_t attn_step_column(int kk) { return (kk / 4) * 64 + 8 * (kk % 4); }
 
 // 64 columns of one warp's lanes to registers.
 __device__ __forceinline__ void attn_ld64(uint32_t taddr, uint32_t (&v)[2][32]) {
   tmem_ld32(taddr, v[0]);
   tmem_ld32(taddr + 32, v[1]);
   tmem_wait_ld();
-}
-
-// The warp's stores to tensor memory are done: tell the MMA warp.
-__device__ __forceinline__ void attn_publish(uint64_t* bar, int lane) {
-  tmem_wait_st();
-  tc_fence_before();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(bar);
 }
 
 // ---------------------------------------------------------------------------
@@ -94,7 +89,7 @@ struct AttnDkvCfg {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = kAttnTile * D * 2;
   static constexpr int kStages = D == 128 ? 2 : 4;         // of Q, and of dO
-  static constexpr int kBars = 6 * kStages + 2 * kStages + 1 + 4 + 1;
+  static constexpr int kBars = 6 * kStages + 2 * kStages + 1 + 6 + 1;
   static constexpr int kSmemBytes = (2 + 2 * kStages) * kTileBytes + kStages * kAttnTile * 8 + kBars * 8 + 16 + 1024;
   static_assert(kSmemBytes <= kSmemLimitBytes, "shared memory");
 };
@@ -121,10 +116,10 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
   uint64_t* st_empty = st_full + S;
   uint64_t* kv_full = st_empty + S;
   uint64_t* s_full = kv_full + 1;
-  uint64_t* p_full = s_full + 1;
-  uint64_t* dp_full = p_full + 1;
-  uint64_t* ds_full = dp_full + 1;
-  uint64_t* mma_done = ds_full + 1;
+  uint64_t* p_full = s_full + 1;       // [2] quarters of P from both warpgroups
+  uint64_t* dp_full = p_full + 2;
+  uint64_t* ds_full = dp_full + 1;     // [2]
+  uint64_t* mma_done = ds_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   AbortCtl ctl{abort_flag, p.plan.head};
@@ -139,9 +134,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     }
     mbar_init(kv_full, 1);
     mbar_init(s_full, 1);
-    mbar_init(p_full, 8);
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, 8);
+    for (int c = 0; c < 2; ++c) { mbar_init(&p_full[c], 8); mbar_init(&ds_full[c], 8); }
     mbar_init(mma_done, 1);
     *abort_flag = 0u;
     fence_mbar_init();
@@ -205,70 +199,78 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       }
     } else if (warp == 1) {
       // -------------------------------------------------------------- MMA
-      if (lane == 0) {
-        constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
-        constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
-        // A (keys, resident) times a ring tile's rows
-        auto across = [&](uint8_t* a, uint8_t* b, uint32_t d) {
-          const uint32_t sa = smem_u32(a), sb = smem_u32(b);
+      constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
+      constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
+      // A (keys, resident) times a ring tile's rows
+      auto across = [&](uint64_t a, const uint8_t* ring, uint32_t stage, uint32_t d) {
+        const uint64_t b = sdesc_sw128(smem_u32(ring), 16, 1024) + stage * (C::kTileBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / 4) * (T * 128) + (kk % 4) * 32;
-            mma_bf16(d, sdesc_sw128(sa + off, 16, 1024), sdesc_sw128(sb + off, 16, 1024), kIdS, kk > 0);
+            const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
+            mma_bf16(d, a + off, b + off, kIdS, kk > 0);
           }
-        };
-        // tensor memory (keys x queries) times a ring tile
-        auto along = [&](uint32_t a, uint8_t* b, uint32_t d, bool fresh) {
-          const uint32_t sb = smem_u32(b);
+        }
+      };
+      // tensor memory (keys x queries) times a ring tile
+      auto along = [&](uint32_t a, uint64_t* ready, uint32_t parity, const uint8_t* ring, uint32_t stage, uint32_t d,
+                       bool fresh) {
+        const uint64_t b = sdesc_sw128(smem_u32(ring), T * 128, 1024) + stage * (C::kTileBytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < T / 16; ++kk)
-            mma_bf16_ta(d, attn_half_step(a, kk), sdesc_sw128(sb + kk * 2048, T * 128, 1024), kIdO, !fresh || kk > 0);
-        };
-        RingPos r;
-        bool ok = mbar_wait(kv_full, 0, ctl) && mbar_wait(&q_full[0], 0, ctl);
-        if (ok) {
+        for (int c = 0; c < 2; ++c) {
+          if (!mbar_wait_warp(&ready[c], parity, ctl)) return false;
           tc_fence_after();
-          across(sk, ring_q, tS);
-          mma_commit(s_full);
-          ok = mbar_wait(&o_full[0], 0, ctl);
-        }
-        if (ok) {
-          tc_fence_after();
-          across(sv, ring_o, tP);
-          mma_commit(dp_full);
-        }
-        for (int i = 0; i < n && ok; ++i) {
-          RingPos nx = r;
-          nx.next(S);
-          ok = mbar_wait(p_full, i & 1, ctl);
-          if (!ok) break;
-          tc_fence_after();
-          along(tS, ring_o + r.stage * C::kTileBytes, tV, i == 0);
-          mma_commit(&o_empty[r.stage]);
-          if (i + 1 < n) {
-            ok = mbar_wait(&q_full[nx.stage], nx.phase, ctl);
-            if (!ok) break;
-            tc_fence_after();
-            across(sk, ring_q + nx.stage * C::kTileBytes, tS);
-            mma_commit(s_full);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < T / 32; ++k) {
+              const int kk = attn_part_step(c, k);
+              mma_bf16_ta(d, a + attn_step_column(kk), b + kk * (2048 >> 4), kIdO, !fresh || c + k > 0);
+            }
           }
-          ok = mbar_wait(ds_full, i & 1, ctl);
-          if (!ok) break;
-          tc_fence_after();
-          along(tP, ring_q + r.stage * C::kTileBytes, tK, i == 0);
-          mma_commit(&q_empty[r.stage]);
-          if (i + 1 < n) {
-            ok = mbar_wait(&o_full[nx.stage], nx.phase, ctl);
-            if (!ok) break;
-            tc_fence_after();
-            across(sv, ring_o + nx.stage * C::kTileBytes, tP);
-            mma_commit(dp_full);
-          }
-          r = nx;
         }
-        mma_commit(mma_done);
-        mbar_wait(mma_done, 0, quiet);
+        return true;
+      };
+      const uint64_t k_desc = sdesc_sw128(smem_u32(sk), 16, 1024), v_desc = sdesc_sw128(smem_u32(sv), 16, 1024);
+      RingPos r;
+      bool ok = mbar_wait_warp(kv_full, 0, ctl) && mbar_wait_warp(&q_full[0], 0, ctl);
+      if (ok) {
+        tc_fence_after();
+        across(k_desc, ring_q, 0, tS);
+        if (elect_one()) mma_commit(s_full);
+        ok = mbar_wait_warp(&o_full[0], 0, ctl);
       }
+      if (ok) {
+        tc_fence_after();
+        across(v_desc, ring_o, 0, tP);
+        if (elect_one()) mma_commit(dp_full);
+      }
+      for (int i = 0; i < n && ok; ++i) {
+        RingPos nx = r;
+        nx.next(S);
+        ok = along(tS, p_full, i & 1, ring_o, r.stage, tV, i == 0);
+        if (!ok) break;
+        if (elect_one()) mma_commit(&o_empty[r.stage]);
+        if (i + 1 < n) {
+          ok = mbar_wait_warp(&q_full[nx.stage], nx.phase, ctl);
+          if (!ok) break;
+          tc_fence_after();
+          across(k_desc, ring_q, nx.stage, tS);
+          if (elect_one()) mma_commit(s_full);
+        }
+        ok = along(tP, ds_full, i & 1, ring_q, r.stage, tK, i == 0);
+        if (!ok) break;
+        if (elect_one()) mma_commit(&q_empty[r.stage]);
+        if (i + 1 < n) {
+          ok = mbar_wait_warp(&o_full[nx.stage], nx.phase, ctl);
+          if (!ok) break;
+          tc_fence_after();
+          across(v_desc, ring_o, nx.stage, tP);
+          if (elect_one()) mma_commit(dp_full);
+        }
+        r = nx;
+      }
+      if (elect_one()) mma_commit(mma_done);
+      mbar_wait_warp(mma_done, 0, quiet);
     } else if (warp == 2) {
       // -------------------------------------------------------------- row statistics
       // Rows past the document: lse = infinity makes their p zero.
@@ -338,8 +340,10 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       tc_fence_after();
       const float* st = stat + r.stage * 2 * T + 64 * half;
       uint32_t v[2][32];
-      float g[2][32];                   // p, then p d(cap tanh)
+      float2 g[32];                     // p, then p d(cap tanh)
       attn_ld64(rS, v);
+      score.template apply<2, true, true>(v, i0 - key, g);
+      const float2 mul = both(score.mul);
       const bool part = !all_keys && i0 - 64 * half < t.row0 + T;
       const int lim = key < t.prefix_end ? 0 : key - i0;             // queries from this one on see the key
 #pragma unroll
@@ -348,23 +352,28 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           const float4 l = *reinterpret_cast<const float4*>(st + 32 * c + e);
-          const float ls[4] = {l.x, l.y, l.z, l.w};
+          const float2 nl[2] = {make_float2(-l.x, -l.y), make_float2(-l.z, -l.w)};
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            float th;
-            const float z = score.one(__uint_as_float(v[c][e + u]), static_cast<float>(i0 - key + 32 * c + e + u), &th);
-            float pr = ex2(fmaf(z, score.mul, -ls[u]));
-            if (part && 32 * c + e + u < lim) pr = 0.0f;
-            v[c][e + u] = __float_as_uint(pr);
-            g[c][e + u] = pr;
-            if constexpr (kCap) g[c][e + u] *= fmaf(-th, th, 1.0f);
+          for (int u = 0; u < 2; ++u) {
+            const int i = 16 * c + e / 2 + u;
+            const float2 y = attn_exp2<kAttnBwdPoly>(fma2(pair_of(&v[c][e + 2 * u]), mul, nl[u]), i);
+            AttnScore<kCap, kBias>::put(v[c], e + 2 * u, y);
           }
-          w[e / 2] = pack_bf16x2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
-          w[e / 2 + 1] = pack_bf16x2(__uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3]));
+        }
+        if (part) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (32 * c + e < lim) v[c][e] = 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 y = pair_of(&v[c][e]);
+          w[e / 2] = pack_bf16x2(y.x, y.y);
+          g[16 * c + e / 2] = kCap ? mul2(y, g[16 * c + e / 2]) : y;
         }
         tmem_st16(rS + 16 * c, w);
+        attn_publish(&p_full[c], lane);
       }
-      attn_publish(p_full, lane);
       ok = __all_sync(0xffffffffu, mbar_wait(dp_full, i & 1, ctl));
       if (!ok) break;
       tc_fence_after();
@@ -375,14 +384,14 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           const float4 d = *reinterpret_cast<const float4*>(st + T + 32 * c + e);
-          w[e / 2] = pack_bf16x2(g[c][e] * (__uint_as_float(v[c][e]) - d.x),
-                                 g[c][e + 1] * (__uint_as_float(v[c][e + 1]) - d.y));
-          w[e / 2 + 1] = pack_bf16x2(g[c][e + 2] * (__uint_as_float(v[c][e + 2]) - d.z),
-                                     g[c][e + 3] * (__uint_as_float(v[c][e + 3]) - d.w));
+          const float2 a = mul2(g[16 * c + e / 2], add2(pair_of(&v[c][e]), make_float2(-d.x, -d.y)));
+          const float2 b = mul2(g[16 * c + e / 2 + 1], add2(pair_of(&v[c][e + 2]), make_float2(-d.z, -d.w)));
+          w[e / 2] = pack_bf16x2(a.x, a.y);
+          w[e / 2 + 1] = pack_bf16x2(b.x, b.y);
         }
         tmem_st16(rP + 16 * c, w);
+        attn_publish(&ds_full[c], lane);
       }
-      attn_publish(ds_full, lane);
       if (lane == 0) mbar_arrive(&st_empty[r.stage]);
       r.next(S);
     }
@@ -533,55 +542,59 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       }
     } else if (warp == 1) {
       // -------------------------------------------------------------- MMA
-      if (lane == 0) {
-        constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
-        constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
-        auto across = [&](uint8_t* a, uint8_t* b, uint32_t d) {
-          const uint32_t sa = smem_u32(a), sb = smem_u32(b);
+      constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
+      constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
+      auto across = [&](const uint8_t* a, const uint8_t* ring, uint32_t stage, uint32_t d) {
+        const uint64_t ad = sdesc_sw128(smem_u32(a), 16, 1024);
+        const uint64_t b = sdesc_sw128(smem_u32(ring), 16, 1024) + stage * (C::kTileBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / 4) * (T * 128) + (kk % 4) * 32;
-            mma_bf16(d, sdesc_sw128(sa + off, 16, 1024), sdesc_sw128(sb + off, 16, 1024), kIdS, kk > 0);
+            const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
+            mma_bf16(d, ad + off, b + off, kIdS, kk > 0);
           }
-        };
-        RingPos ks, kd, v;             // K tiles of the scores, of dQ; V tiles
-        bool ok = mbar_wait(qo_full, 0, ctl);
-        auto scores = [&](int j) {
-          if (!mbar_wait(&k_full[ks.stage], ks.phase, ctl)) return false;
-          tc_fence_after();
-          across(sq, ring_k + ks.stage * C::kTileBytes, tS + (j & 1) * T);
-          mma_commit(&s_full[j & 1]);
-          ks.next(SK);
-          return true;
-        };
-        auto values = [&]() {
-          if (!mbar_wait(&v_full[v.stage], v.phase, ctl)) return false;
-          tc_fence_after();
-          across(so, ring_v + v.stage * C::kTileBytes, tP);
-          mma_commit(dp_full);
-          mma_commit(&v_empty[v.stage]);
-          v.next(SV);
-          return true;
-        };
-        ok = ok && scores(0) && values();
-        if (n > 1) ok = ok && scores(1);
-        for (int j = 0; j < n && ok; ++j) {
-          ok = mbar_wait(ds_full, j & 1, ctl);
-          if (!ok) break;
-          tc_fence_after();
-          if (j + 1 < n) ok = values();
-          if (!ok) break;
-          const uint32_t sb = smem_u32(ring_k + kd.stage * C::kTileBytes), a = tS + (j & 1) * T;
+        }
+      };
+      RingPos ks, kd, v;             // K tiles of the scores, of dQ; V tiles
+      auto scores = [&](int j) {
+        if (!mbar_wait_warp(&k_full[ks.stage], ks.phase, ctl)) return false;
+        tc_fence_after();
+        across(sq, ring_k, ks.stage, tS + (j & 1) * T);
+        if (elect_one()) mma_commit(&s_full[j & 1]);
+        ks.next(SK);
+        return true;
+      };
+      auto values = [&]() {
+        if (!mbar_wait_warp(&v_full[v.stage], v.phase, ctl)) return false;
+        tc_fence_after();
+        across(so, ring_v, v.stage, tP);
+        if (elect_one()) mma_commit(dp_full);
+        if (elect_one()) mma_commit(&v_empty[v.stage]);
+        v.next(SV);
+        return true;
+      };
+      bool ok = mbar_wait_warp(qo_full, 0, ctl);
+      ok = ok && scores(0) && values();
+      if (n > 1) ok = ok && scores(1);
+      for (int j = 0; j < n && ok; ++j) {
+        ok = mbar_wait_warp(ds_full, j & 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        if (j + 1 < n) ok = values();
+        if (!ok) break;
+        const uint64_t b = sdesc_sw128(smem_u32(ring_k), T * 128, 1024) + kd.stage * (C::kTileBytes >> 4);
+        const uint32_t a = tS + (j & 1) * T;
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < T / 16; ++kk)
-            mma_bf16_ta(tQ, attn_half_step(a, kk), sdesc_sw128(sb + kk * 2048, T * 128, 1024), kIdO, j > 0 || kk > 0);
-          mma_commit(&k_empty[kd.stage]);
-          kd.next(SK);
-          if (j + 2 < n) ok = scores(j + 2);
+            mma_bf16_ta(tQ, a + attn_step_column(kk), b + kk * (2048 >> 4), kIdO, j > 0 || kk > 0);
         }
-        mma_commit(mma_done);
-        mbar_wait(mma_done, 0, quiet);
+        if (elect_one()) mma_commit(&k_empty[kd.stage]);
+        kd.next(SK);
+        if (j + 2 < n) ok = scores(j + 2);
       }
+      if (elect_one()) mma_commit(mma_done);
+      mbar_wait_warp(mma_done, 0, quiet);
     }
   } else if (live && !behind) {
     // ---------------------------------------------------------------- elementwise
@@ -595,6 +608,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     const float lse2 = mine ? p.stat[static_cast<size_t>(h) * p.M + row] : INFINITY;
     const float delta = mine ? p.stat[static_cast<size_t>(p.heads + h) * p.M + row] : 0.0f;
     const AttnScore<kCap, kBias> score(p, h);
+    const float2 mul = both(score.mul), shift = both(-lse2);
     bool ok = true;
     for (int j = 0; j < n && ok; ++j) {
       const int j0 = t.begin + j * T + 64 * half;                        // the first of this thread's 64 keys
@@ -603,20 +617,25 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       if (!ok) break;
       tc_fence_after();
       uint32_t v[2][32];
-      float g[2][32];
+      float2 g[32];                     // p d(cap tanh)
       attn_ld64(rS, v);
-      const bool part = j0 + 64 > all;
-      const int lim = see - j0;
+      score.template apply<2, true, true>(v, j0 - row, g);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          float th;
-          const float z = score.one(__uint_as_float(v[c][e]), static_cast<float>(row - j0 - 32 * c - e), &th);
-          g[c][e] = ex2(fmaf(z, score.mul, -lse2));
-          if constexpr (kCap) g[c][e] *= fmaf(-th, th, 1.0f);
-          if (part && 32 * c + e >= lim) g[c][e] = 0.0f;
+        for (int e = 0; e < 32; e += 2) {
+          const int i = 16 * c + e / 2;
+          const float2 y = attn_exp2<kAttnBwdPoly>(fma2(pair_of(&v[c][e]), mul, shift), i);
+          g[i] = kCap ? mul2(y, g[i]) : y;
         }
+      if (j0 + 64 > all) {
+        const int lim = see - j0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          if (2 * i >= lim) g[i].x = 0.0f;
+          if (2 * i + 1 >= lim) g[i].y = 0.0f;
+        }
+      }
       ok = __all_sync(0xffffffffu, mbar_wait(dp_full, j & 1, ctl));
       if (!ok) break;
       tc_fence_after();
@@ -625,9 +644,10 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       for (int c = 0; c < 2; ++c) {
         uint32_t w[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2)
-          w[e / 2] = pack_bf16x2(g[c][e] * (__uint_as_float(v[c][e]) - delta),
-                                 g[c][e + 1] * (__uint_as_float(v[c][e + 1]) - delta));
+        for (int e = 0; e < 32; e += 2) {
+          const float2 y = mul2(g[16 * c + e / 2], add2(pair_of(&v[c][e]), both(-delta)));
+          w[e / 2] = pack_bf16x2(y.x, y.y);
+        }
         tmem_st16(rS + 16 * c, w);
       }
       attn_publish(ds_full, lane);

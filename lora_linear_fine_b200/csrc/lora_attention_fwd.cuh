@@ -26,7 +26,7 @@ struct AttnFwdCfg {
   static constexpr int kBoxes = D / 64;                          // 128-byte column boxes of a tile
   static constexpr int kTileBytes = kAttnTile * D * 2;
   static constexpr int kStages = D == 128 ? 4 : 8;               // K and V tiles in flight
-  static constexpr int kBars = 2 * kStages + 1 + 1 + 2 + 2 + 2 + 1;
+  static constexpr int kBars = 2 * kStages + 1 + 1 + 2 + 4 + 2 + 1;
   static constexpr int kSmemBytes = (2 + kStages) * kTileBytes + kBars * 8 + 16 + 1024;
   static_assert(kSmemBytes <= kSmemLimitBytes, "shared memory");
 };
@@ -34,6 +34,7 @@ struct AttnFwdCfg {
 // the first warpgroup and 200 for the softmax ones, whose row of 128 scores
 // stays in registers.
 constexpr int kAttnFwdRegsLow = 104, kAttnFwdRegsHigh = 200;
+constexpr int kAttnFwdPoly = 1;          // of four pairs of exponentials, those by the polynomial
 constexpr int kAttnFwdThreads = 384;     // warps: TMA, MMA, two idle, softmax of tile a (4), of tile b (4)
 
 struct AttnFwdMaps {
@@ -53,8 +54,8 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
   uint64_t* q_full = empty + S;
   uint64_t* land = q_full + 1;       // a tile that is trimmed before it counts as full
   uint64_t* s_full = land + 1;       // [2] S of this key tile is in tensor memory
-  uint64_t* p_full = s_full + 2;     // [2] P is in tensor memory (and O rescaled)
-  uint64_t* pv_done = p_full + 2;    // [2] O holds this key tile
+  uint64_t* p_full = s_full + 2;     // [2][2] that half of P is in tensor memory (and O rescaled)
+  uint64_t* pv_done = p_full + 4;    // [2] O holds this key tile
   uint64_t* mma_done = pv_done + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile uint32_t* abort_flag = tmem_slot + 1;
@@ -66,7 +67,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
     for (int i = 0; i < S; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
     mbar_init(q_full, 1);
     mbar_init(land, 1);
-    for (int x = 0; x < 2; ++x) { mbar_init(&s_full[x], 1); mbar_init(&p_full[x], 4); mbar_init(&pv_done[x], 1); }
+    for (int x = 0; x < 2; ++x) { mbar_init(&s_full[x], 1); mbar_init(&p_full[2 * x], 4); mbar_init(&p_full[2 * x + 1], 4); mbar_init(&pv_done[x], 1); }
     mbar_init(mma_done, 1);
     *abort_flag = 0u;
     fence_mbar_init();
@@ -144,60 +145,72 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA
-      if (lane == 0) {
-        constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
-        constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
-        auto scores = [&](int x, uint32_t stage) {
-          const uint32_t sq = smem_u32(smem + x * C::kTileBytes), sk = smem_u32(ring + stage * C::kTileBytes);
-  #pragma unroll
+      constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
+      constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
+      const uint64_t q_desc = sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(ring), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(ring), T * 128, 1024);
+      auto scores = [&](int x, uint32_t stage) {
+        const uint64_t a = q_desc + x * (C::kTileBytes >> 4), b = k_desc + stage * (C::kTileBytes >> 4);
+        if (elect_one()) {
+#pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / 4) * (T * 128) + (kk % 4) * 32;
-            mma_bf16(tbase + x * T, sdesc_sw128(sq + off, 16, 1024), sdesc_sw128(sk + off, 16, 1024), kIdS, kk > 0);
+            const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
+            mma_bf16(tbase + x * T, a + off, b + off, kIdS, kk > 0);
           }
-          mma_commit(&s_full[x]);
-        };
-        auto values = [&](int x, uint32_t stage, bool first) {
-          const uint32_t sv = smem_u32(ring + stage * C::kTileBytes);
-  #pragma unroll
-          for (int kk = 0; kk < T / 16; ++kk)
-            mma_bf16_ta(tbase + 256 + x * T, tbase + x * T + 8 * kk, sdesc_sw128(sv + kk * 2048, T * 128, 1024), kIdO,
-                        !first || kk > 0);
-          mma_commit(&pv_done[x]);
-        };
-        RingPos rp;
-        bool ok = mbar_wait(q_full, 0, ctl) && mbar_wait(&full[0], 0, ctl);
-        tc_fence_after();
-        if (ok) {
-          for (int x = 0; x < tiles_x; ++x) scores(x, 0);
-          mma_commit(&empty[0]);
+        }
+        if (elect_one()) mma_commit(&s_full[x]);
+      };
+      // half of the keys: 4 steps of 16
+      auto values = [&](int x, uint32_t stage, int half, bool first) {
+        const uint64_t b = v_desc + stage * (C::kTileBytes >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < T / 32; ++k) {
+            const int kk = half * (T / 32) + k;
+            mma_bf16_ta(tbase + 256 + x * T, tbase + x * T + 8 * kk, b + kk * (2048 >> 4), kIdO, !first || kk > 0);
+          }
+        }
+      };
+      RingPos rp;
+      bool ok = mbar_wait_warp(q_full, 0, ctl) && mbar_wait_warp(&full[0], 0, ctl);
+      tc_fence_after();
+      if (ok) {
+        for (int x = 0; x < tiles_x; ++x) scores(x, 0);
+        if (elect_one()) mma_commit(&empty[0]);
+        rp.next(S);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const RingPos v = rp;
+        ok = mbar_wait_warp(&full[v.stage], v.phase, ctl);
+        rp.next(S);
+        const RingPos k = rp;
+        if (ok && j + 1 < n) {
+          ok = mbar_wait_warp(&full[k.stage], k.phase, ctl);
           rp.next(S);
         }
-        for (int j = 0; j < n && ok; ++j) {
-          const RingPos v = rp;
-          ok = mbar_wait(&full[v.stage], v.phase, ctl);
-          rp.next(S);
-          const RingPos k = rp;
-          if (ok && j + 1 < n) {
-            ok = mbar_wait(&full[k.stage], k.phase, ctl);
-            rp.next(S);
-          }
-          for (int x = 0; x < tiles_x && ok; ++x) {
-            const int nx = x == 0 ? n_a : n;
-            if (j >= nx) continue;
-            ok = mbar_wait(&p_full[x], j & 1, ctl);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int nx = x == 0 ? n_a : (tiles_x == 2 ? n : 0);
+          if (!ok || j >= nx) continue;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            ok = ok && mbar_wait_warp(&p_full[2 * x + half], j & 1, ctl);
             if (!ok) break;
             tc_fence_after();
-            values(x, v.stage, j == 0);
-            if (j + 1 < nx) scores(x, k.stage);
+            values(x, v.stage, half, j == 0);
           }
-          if (ok) {
-            mma_commit(&empty[v.stage]);
-            if (j + 1 < n) mma_commit(&empty[k.stage]);
-          }
+          if (!ok) continue;
+          if (elect_one()) mma_commit(&pv_done[x]);
+          if (j + 1 < nx) scores(x, k.stage);
         }
-        mma_commit(mma_done);
-        mbar_wait(mma_done, 0, quiet);
+        if (ok) {
+          if (elect_one()) mma_commit(&empty[v.stage]);
+          if (j + 1 < n) if (elect_one()) mma_commit(&empty[k.stage]);
+        }
       }
+      if (elect_one()) mma_commit(mma_done);
+      mbar_wait_warp(mma_done, 0, quiet);
     }
   } else if (live && !behind) {
     regs_raise<kAttnFwdRegsHigh>();
@@ -210,7 +223,8 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
     const int see = min(max(row + 1, t.prefix_end), t.end);              // keys [begin, see)
     const int all = min(max(t.row0 + x * T + 1, t.prefix_end), t.end);   // ... that every row sees
     const AttnScore<kCap, kBias> score(p, h);
-    float m = -INFINITY, l = 0.0f;
+    float m = -INFINITY;
+    float2 l = make_float2(0.0f, 0.0f);      // two partial sums
     bool ok = true;
     for (int j = 0; j < nx && ok; ++j) {
       const int j0 = t.begin + j * T;
@@ -219,24 +233,24 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
       if (!ok) break;
       tc_fence_after();
       uint32_t v[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, v[c]);
+      tmem_ld32(tS, v[0]);
+      tmem_ld32(tS + 32, v[1]);
+      tmem_ld32(tS + 64, v[2]);
+      tmem_ld32(tS + 96, v[3]);
       tmem_wait_ld();
-      score.apply(v, row - j0);
+      score.template apply<4, true, false>(v, j0 - row, nullptr);
       if (j0 + T > all) {
         const int lim = see - j0;
 #pragma unroll
         for (int c = 0; c < T; ++c)
           if (c >= lim) v[c / 32][c % 32] = 0xff800000u;                  // -infinity
       }
-      float top[4];
+      float top[4] = {m, m, m, m};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        top[c] = __uint_as_float(v[c][0]);
+      for (int e = 0; e < 32; e += 2)
 #pragma unroll
-        for (int e = 1; e < 32; ++e) top[c] = fmaxf(top[c], __uint_as_float(v[c][e]));
-      }
-      const float mx = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+        for (int c = 0; c < 4; ++c) top[c] = max3(top[c], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+      const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
       if (j == 0) {
         m = mx;
       } else {
@@ -246,7 +260,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const float a = grow ? ex2((m - mx) * score.mul) : 1.0f;
-          l *= a;
+          l = mul2(l, both(a));
           if (grow) m = mx;
 #pragma unroll
           for (int c = 0; c < D; c += 32) {
@@ -259,31 +273,31 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
           }
         }
       }
-      // a row without a finite score so far: exp2(-inf - 0) = 0 throughout
-      const float shift = m == -INFINITY ? 0.0f : -m * score.mul;
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      // a row without a finite score so far has no p yet
+      const bool none = m == -INFINITY;
+      const float2 shift = both(none ? 0.0f : -m * score.mul), mul = both(score.mul);
+      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float a = ex2(fmaf(__uint_as_float(v[c][e]), score.mul, shift));
-          const float b = ex2(fmaf(__uint_as_float(v[c][e + 1]), score.mul, shift));
-          sum[(e / 2) & 3] += a + b;
-          w[e / 2] = pack_bf16x2(a, b);
+          const float2 y = attn_exp2<kAttnFwdPoly>(fma2(pair_of(&v[c][e]), mul, shift), e / 2);
+          sum[(e / 2) & 1] = add2(sum[(e / 2) & 1], y);
+          w[e / 2] = pack_bf16x2(y.x, y.y);
         }
         tmem_st16(tS + 16 * c, w);
+        // the tensor core begins with the first half of the keys
+        if (c == 1) attn_publish(&p_full[2 * x], lane);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[x]);
+      attn_publish(&p_full[2 * x + 1], lane);
+      if (none) sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+      l = add2(l, add2(sum[0], sum[1]));
     }
     if (ok && nx > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[x], (nx - 1) & 1, ctl));
     if (ok && nx > 0) {
       tc_fence_after();
-      const float inv = 1.0f / l;
+      const float total = l.x + l.y, inv = 1.0f / total;
       const bool mine = row < t.end;
       __nv_bfloat16* out = p.O + (static_cast<size_t>(row) * p.heads + h) * D;
 #pragma unroll
@@ -294,7 +308,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
         if (mine) attn_store32(out + c, o, inv);
       }
       // natural logarithm of sum exp z
-      if (mine) p.lse[static_cast<size_t>(row) * p.heads + h] = (m * score.mul + log2f(l)) * 0.69314718056f;
+      if (mine) p.lse[static_cast<size_t>(row) * p.heads + h] = (m * score.mul + log2f(total)) * 0.69314718056f;
     }
   }
 
