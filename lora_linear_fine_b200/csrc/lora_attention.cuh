@@ -162,6 +162,38 @@ __device__ __forceinline__ bool attn_plan_ok(const AttnParams& p) {
   return false;
 }
 
+// What a persistent CTA works on: (tile, head) pairs, the heads of a tile next
+// to each other, tiles in falling order of their work.  The CTAs take them in
+// rounds whose direction alternates, so that the sums of their work stay close.
+// Each role of a CTA walks over the same items; the next one's tile is loaded
+// while it is at the one before.
+struct AttnItems {
+  AttnTileRef t;
+  int h;
+  __device__ __forceinline__ AttnItems(const AttnTileRef* list, uint32_t tiles, int heads)
+      : t{0, 0, 0, 0}, h(0), list_(list), heads_(static_cast<uint32_t>(heads)), total_(tiles * heads_) {
+    fetch();
+  }
+  __device__ __forceinline__ bool advance() {
+    if (at_ >= total_) return false;
+    t = next_;
+    h = static_cast<int>(at_ % heads_);
+    ++round_;
+    fetch();
+    return true;
+  }
+  __device__ __forceinline__ bool behind() const { return t.prefix_end < 0; }
+
+ private:
+  __device__ __forceinline__ void fetch() {
+    at_ = round_ * gridDim.x + ((round_ & 1u) ? gridDim.x - 1u - blockIdx.x : blockIdx.x);
+    if (at_ < total_) next_ = list_[at_ / heads_];
+  }
+  const AttnTileRef* list_;
+  uint32_t heads_, total_, round_ = 0, at_ = 0;
+  AttnTileRef next_{0, 0, 0, 0};
+};
+
 // Key tiles that the `rows` rows from row0 on see.
 __device__ __forceinline__ int attn_key_tiles(const AttnTileRef& t, int row0, int rows) {
   const int see = max(min(row0 + rows, t.end), t.prefix_end);
@@ -239,14 +271,14 @@ __device__ __forceinline__ float2 attn_exp2(float2 x, int i) {
 template <bool kCap, bool kBias>
 struct AttnScore {
   float mul;
-  float headroom;   // 8 / mul: how far values may outgrow the running maximum
+  float headroom;   // 16 / mul: how far values may outgrow the running reference
   float pre, cap2, slope2;
   __device__ __forceinline__ AttnScore(const AttnParams& p, int h) {
     cap2 = kCap ? p.cap * kLog2e : 0.0f;
     pre = kCap ? p.scale / p.cap : p.scale * kLog2e;
     slope2 = kBias ? p.slopes[h] * kLog2e : 0.0f;
     mul = kBias ? 1.0f : kCap ? cap2 : pre;
-    headroom = 8.0f / mul;
+    headroom = 16.0f / mul;
   }
   // 32 kChunks products of a row in place; dist0 = distance (either sign) of
   // the first, rising by 1 (kUp) or falling by 1 from one to the next.
@@ -308,18 +340,27 @@ struct AttnScore {
   }
 };
 
-// 32 registers that a tmem load fills are read after this point only.
-__device__ __forceinline__ void attn_hold(uint32_t (&v)[32]) {
-#pragma unroll
-  for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(v[e]));
-}
-
 // The warp's stores to tensor memory are done: tell the MMA warp.
 __device__ __forceinline__ void attn_publish(uint64_t* bar, int lane) {
   tmem_wait_st();
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
+}
+
+// A tile of 128 rows x 128 scores is worked on by 128 threads a group of kCols
+// columns; each group writes its bf16 results over the first half of its own
+// columns, in two parts.  Part c of all groups is four of the eight steps of 16
+// that the product over them takes: k = 0 .. 3 -> step, step -> column.
+template <int kCols>
+__device__ __forceinline__ int attn_part_step(int c, int k) {
+  constexpr int n = kCols / 32;          // steps of a part in a group
+  return (k / n) * 2 * n + n * c + k % n;
+}
+template <int kCols>
+__device__ __forceinline__ uint32_t attn_step_column(int kk) {
+  constexpr int n = kCols / 16;
+  return (kk / n) * kCols + 8 * (kk % n);
 }
 
 // Zeroes rows [first, kAttnTile) of a tile of kBoxes 128-byte column boxes in
@@ -334,37 +375,38 @@ __device__ __forceinline__ void attn_trim_tile(uint8_t* tile, int first, int lan
   __syncwarp();
 }
 
-// Waits for the last fill of every ring stage that has one (the aborting
-// producer's copies in flight); rp: the stage it would fill next.
+// Waits for the last fill of every ring stage (the aborting producer's copies
+// in flight); rp: the stage it would fill next.  A stage without a fill passes.
 __device__ __forceinline__ void attn_drain(uint64_t* full, int stages, RingPos rp) {
   volatile uint32_t never = 0u;
   const AbortCtl quiet{&never, nullptr};
-  for (int i = 0; i < stages; ++i) {
-    if (i < static_cast<int>(rp.stage)) mbar_wait(&full[i], rp.phase, quiet);
-    else if (rp.phase != 0u) mbar_wait(&full[i], rp.phase ^ 1u, quiet);
-  }
+  for (int i = 0; i < stages; ++i)
+    mbar_wait(&full[i], i < static_cast<int>(rp.stage) ? rp.phase : rp.phase ^ 1u, quiet);
 }
 
-// Rows [first, last) of one head's columns of out [M x heads * D] become zero.  Whole CTA.
+// Rows [first, last) of one head's columns of out [M x heads * D] become zero.
+// Thread i of n.
 template <int D>
-__device__ __forceinline__ void attn_zero_rows(__nv_bfloat16* out, int heads, int h, int first, int last) {
-  const int n = (last - first) * (D / 8);
-  for (int i = threadIdx.x; i < n; i += blockDim.x)
+__device__ __forceinline__ void attn_zero_rows(__nv_bfloat16* out, int heads, int h, int first, int last, int i, int n) {
+  for (; i < (last - first) * (D / 8); i += n)
     reinterpret_cast<uint4*>(out + (static_cast<size_t>(first + i / (D / 8)) * heads + h) * D)[i % (D / 8)] =
         make_uint4(0u, 0u, 0u, 0u);
 }
 
-// 32 fp32 values times `by` as bf16.
-__device__ __forceinline__ void attn_store32(__nv_bfloat16* out, const uint32_t (&v)[32], float by) {
+// fp32 values times `by` as bf16.
+__device__ __forceinline__ uint4 attn_pack8(const uint32_t* v, float by) {
+  uint32_t w[4];
 #pragma unroll
-  for (int e = 0; e < 32; e += 8) {
-    uint4 w;
-    w.x = pack_bf16x2(__uint_as_float(v[e]) * by, __uint_as_float(v[e + 1]) * by);
-    w.y = pack_bf16x2(__uint_as_float(v[e + 2]) * by, __uint_as_float(v[e + 3]) * by);
-    w.z = pack_bf16x2(__uint_as_float(v[e + 4]) * by, __uint_as_float(v[e + 5]) * by);
-    w.w = pack_bf16x2(__uint_as_float(v[e + 6]) * by, __uint_as_float(v[e + 7]) * by);
-    *reinterpret_cast<uint4*>(out + e) = w;
+  for (int k = 0; k < 4; ++k) {
+    const float2 y = mul2(pair_of(v + 2 * k), both(by));
+    w[k] = pack_bf16x2(y.x, y.y);
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int n>
+__device__ __forceinline__ void attn_store(__nv_bfloat16* out, const uint32_t (&v)[n], float by) {
+#pragma unroll
+  for (int e = 0; e < n; e += 8) *reinterpret_cast<uint4*>(out + e) = attn_pack8(&v[e], by);
 }
 
 }  // namespace lora

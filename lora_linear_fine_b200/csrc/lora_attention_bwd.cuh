@@ -15,9 +15,8 @@
 
 namespace lora {
 
-constexpr int kAttnBwdThreads = 384;     // warps: TMA, MMA, statistics, trimming, two warpgroups of elementwise work
+constexpr int kAttnBwdThreads = 640;     // warps: TMA, MMA, statistics, trimming, 16 of elementwise work
 constexpr int kAttnBwdPoly = 1;          // of four pairs of exponentials, those by the polynomial
-constexpr int kAttnBwdRegsLow = 104, kAttnBwdRegsHigh = 200;
 
 struct AttnBwdMaps {
   CUtensorMap q, k, v, d_o;   // [M x heads * D] bf16, box 64 x 128, 128-byte swizzle
@@ -60,27 +59,13 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
   p.stat[static_cast<size_t>(p.heads + h) * p.M + m] = s[threadIdx.x >> 5][threadIdx.x & 31];
 }
 
-// The A operand of dV, dK and dQ is written to tensor memory by two
-// warpgroups, 64 columns of the tile each (the first one's 32 packed columns at
-// `base`, the second one's at base + 64), in two parts of 32.  Part c of both
-// is four steps of 16 out of the product's eight: k = 0 .. 3 -> step.
-__device__ __forceinline__ int attn_part_step(int c, int k) { return (k / 2) * 4 + 2 * c + k % 2; }
-__device__ __forceinline__ uint32_t attn_step_column(int kk) { return (kk / 4) * 64 + 8 * (kk % 4); }
-
-// 64 columns of one warp's lanes to registers.
-__device__ __forceinline__ void attn_ld64(uint32_t taddr, uint32_t (&v)[2][32]) {
-  tmem_ld32(taddr, v[0]);
-  tmem_ld32(taddr + 32, v[1]);
-  tmem_wait_ld();
-}
-
 // ---------------------------------------------------------------------------
 // dk, dv
 // ---------------------------------------------------------------------------
 // For each query head of the group and each query tile i that sees the keys
 // (tiles transposed: rows are keys):
 //   S = K Q_i^T, dP = V dO_i^T      both operands in shared memory
-//   P = exp2(S - lse), dS = P (dP - delta)    256 threads, a row and 64 queries each
+//   P = exp2(S - lse), dS = P (dP - delta)    512 threads, a row and 32 queries each
 //   dV += P dO_i, dK += dS Q_i      P and dS read from tensor memory
 // The products are issued as dV_i, S_i+1, dK_i, dP_i+1: while the elementwise
 // work is at dS_i the tensor core does the first two, at P_i+1 the other two.
@@ -89,8 +74,9 @@ struct AttnDkvCfg {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = kAttnTile * D * 2;
   static constexpr int kStages = D == 128 ? 2 : 4;         // of Q, and of dO
-  static constexpr int kBars = 6 * kStages + 2 * kStages + 1 + 6 + 1;
-  static constexpr int kSmemBytes = (2 + 2 * kStages) * kTileBytes + kStages * kAttnTile * 8 + kBars * 8 + 16 + 1024;
+  static constexpr int kKv = D == 128 ? 1 : 2;             // of K and V
+  static constexpr int kBars = 6 * kStages + 2 * kStages + 2 * kKv + 6 + 2 + 1;
+  static constexpr int kSmemBytes = (2 * kKv + 2 * kStages) * kTileBytes + kStages * kAttnTile * 8 + kBars * 8 + 16 + 1024;
   static_assert(kSmemBytes <= kSmemLimitBytes, "shared memory");
 };
 
@@ -101,9 +87,10 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
   constexpr int T = kAttnTile, S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sk = smem;
-  uint8_t* sv = sk + C::kTileBytes;
-  uint8_t* ring_q = sv + C::kTileBytes;
+  constexpr int NB = C::kKv;
+  uint8_t* sk = smem;                  // [NB]
+  uint8_t* sv = sk + NB * C::kTileBytes;
+  uint8_t* ring_q = sv + NB * C::kTileBytes;
   uint8_t* ring_o = ring_q + S * C::kTileBytes;
   float* stat = reinterpret_cast<float*>(ring_o + S * C::kTileBytes);    // [S][2][T]
   uint64_t* q_full = reinterpret_cast<uint64_t*>(stat + S * 2 * T);
@@ -114,12 +101,15 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
   uint64_t* o_land = q_land + S;
   uint64_t* st_full = o_land + S;
   uint64_t* st_empty = st_full + S;
-  uint64_t* kv_full = st_empty + S;
-  uint64_t* s_full = kv_full + 1;
-  uint64_t* p_full = s_full + 1;       // [2] quarters of P from both warpgroups
+  uint64_t* kv_full = st_empty + S;    // [NB]
+  uint64_t* kv_empty = kv_full + NB;   // [NB]
+  uint64_t* s_full = kv_empty + NB;
+  uint64_t* p_full = s_full + 1;       // [2] parts of P from all warps
   uint64_t* dp_full = p_full + 2;
   uint64_t* ds_full = dp_full + 1;     // [2]
-  uint64_t* mma_done = ds_full + 2;
+  uint64_t* acc_full = ds_full + 2;    // dk and dv of the item are complete
+  uint64_t* acc_empty = acc_full + 1;  // ... and have been read
+  uint64_t* mma_done = acc_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   AbortCtl ctl{abort_flag, p.plan.head};
@@ -130,12 +120,14 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       for (uint64_t* b : {q_full, o_full, q_empty, o_empty, q_land, o_land, st_full}) mbar_init(&b[i], 1);
-      mbar_init(&st_empty[i], 8);
+      mbar_init(&st_empty[i], 16);
     }
-    mbar_init(kv_full, 1);
+    for (int i = 0; i < NB; ++i) { mbar_init(&kv_full[i], 1); mbar_init(&kv_empty[i], 1); }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
-    for (int c = 0; c < 2; ++c) { mbar_init(&p_full[c], 8); mbar_init(&ds_full[c], 8); }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 16);
+    for (int c = 0; c < 2; ++c) { mbar_init(&p_full[c], 16); mbar_init(&ds_full[c], 16); }
     mbar_init(mma_done, 1);
     *abort_flag = 0u;
     fence_mbar_init();
@@ -148,36 +140,23 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
   const uint32_t tK = tbase, tV = tbase + D, tS = tbase + 256, tP = tbase + 384;
   grid_dep_wait();
 
-  const uint32_t tile = blockIdx.x / static_cast<uint32_t>(p.kv_heads);
-  const int hk = static_cast<int>(blockIdx.x - tile * static_cast<uint32_t>(p.kv_heads));
-  const bool live = attn_plan_ok(p) && tile < p.plan.head[kPlanKv];
-  AttnTileRef t{0, 0, 0, 0};
-  if (live) t = p.plan.kv[tile];
-  const bool behind = t.prefix_end < 0;
-  if (behind) {
-    attn_zero_rows<D>(p.dK, p.kv_heads, hk, t.row0, min(t.row0 + T, t.end));
-    attn_zero_rows<D>(p.dV, p.kv_heads, hk, t.row0, min(t.row0 + T, t.end));
-  }
-  // query tiles that see the keys: from the first one with a prefix, else from the keys' own
+  AttnItems items(p.plan.kv, attn_plan_ok(p) ? p.plan.head[kPlanKv] : 0u, p.kv_heads);
   const int group = p.heads / p.kv_heads;
-  const int first = t.row0 < t.prefix_end ? t.begin : t.row0;
-  const int n_tiles = (t.end - first + T - 1) / T;
-  const int n = n_tiles * group;
+  bool ok = true;
+  // query tiles that see the item's keys: from the first one with a prefix, else from the keys' own
+  auto first_of = [&] { return items.t.row0 < items.t.prefix_end ? items.t.begin : items.t.row0; };
 
-  if (live && !behind && warp < 4) {
-    regs_lower<kAttnBwdRegsLow>();
-    if (warp == 0) {
-      // -------------------------------------------------------------- TMA
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA
+    if (lane == 0) {
       RingPos rq;
-      bool ok = true;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(kv_full, 2 * C::kTileBytes);
-        for (int b = 0; b < C::kBoxes; ++b) {
-          tma_load_2d(sk + b * (T * 128), &maps.k, kv_full, hk * D + 64 * b, t.row0);
-          tma_load_2d(sv + b * (T * 128), &maps.v, kv_full, hk * D + 64 * b, t.row0);
-        }
-        for (int i = 0; i < n && ok; ++i) {
-          const int h = hk * group + i / n_tiles, row = first + (i % n_tiles) * T;
+      uint32_t turn = 0;
+      while (ok && items.advance()) {
+        if (items.behind()) continue;
+        const AttnTileRef t = items.t;
+        const int hk = items.h, first = first_of(), n_tiles = (t.end - first + T - 1) / T;
+        int h = hk * group, row = first;
+        for (int i = 0; i < n_tiles * group && ok; ++i) {
           const bool trim = row + T > t.end;
           for (int k = 0; k < 2 && ok; ++k) {
             ok = mbar_wait(k == 0 ? &q_empty[rq.stage] : &o_empty[rq.stage], rq.phase ^ 1u, ctl);
@@ -189,95 +168,119 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             for (int b = 0; b < C::kBoxes; ++b)
               tma_load_2d(dst + b * (T * 128), k == 0 ? &maps.q : &maps.d_o, bar, h * D + 64 * b, row);
           }
-          if (ok) rq.next(S);
-        }
-        if (!ok) {   // every copy has landed before the CTA may end
-          mbar_wait(kv_full, 0, quiet);
-          attn_drain(q_full, S, rq);
-          attn_drain(o_full, S, rq);
-        }
-      }
-    } else if (warp == 1) {
-      // -------------------------------------------------------------- MMA
-      constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
-      constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
-      // A (keys, resident) times a ring tile's rows
-      auto across = [&](uint64_t a, const uint8_t* ring, uint32_t stage, uint32_t d) {
-        const uint64_t b = sdesc_sw128(smem_u32(ring), 16, 1024) + stage * (C::kTileBytes >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
-            mma_bf16(d, a + off, b + off, kIdS, kk > 0);
-          }
-        }
-      };
-      // tensor memory (keys x queries) times a ring tile
-      auto along = [&](uint32_t a, uint64_t* ready, uint32_t parity, const uint8_t* ring, uint32_t stage, uint32_t d,
-                       bool fresh) {
-        const uint64_t b = sdesc_sw128(smem_u32(ring), T * 128, 1024) + stage * (C::kTileBytes >> 4);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (!mbar_wait_warp(&ready[c], parity, ctl)) return false;
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < T / 32; ++k) {
-              const int kk = attn_part_step(c, k);
-              mma_bf16_ta(d, a + attn_step_column(kk), b + kk * (2048 >> 4), kIdO, !fresh || c + k > 0);
+          if (!ok) break;
+          rq.next(S);
+          if (i == 0) {
+            const uint32_t buf = turn % NB;
+            ok = mbar_wait(&kv_empty[buf], ((turn / NB) & 1u) ^ 1u, ctl);
+            if (!ok) break;
+            ++turn;
+            mbar_arrive_expect_tx(&kv_full[buf], 2 * C::kTileBytes);
+            for (int b = 0; b < C::kBoxes; ++b) {
+              tma_load_2d(sk + buf * C::kTileBytes + b * (T * 128), &maps.k, &kv_full[buf], hk * D + 64 * b, t.row0);
+              tma_load_2d(sv + buf * C::kTileBytes + b * (T * 128), &maps.v, &kv_full[buf], hk * D + 64 * b, t.row0);
             }
           }
+          row += T;
+          if (row >= t.end) { row = first; ++h; }
         }
-        return true;
-      };
-      const uint64_t k_desc = sdesc_sw128(smem_u32(sk), 16, 1024), v_desc = sdesc_sw128(smem_u32(sv), 16, 1024);
-      RingPos r;
-      bool ok = mbar_wait_warp(kv_full, 0, ctl) && mbar_wait_warp(&q_full[0], 0, ctl);
-      if (ok) {
-        tc_fence_after();
-        across(k_desc, ring_q, 0, tS);
-        if (elect_one()) mma_commit(s_full);
-        ok = mbar_wait_warp(&o_full[0], 0, ctl);
       }
-      if (ok) {
-        tc_fence_after();
-        across(v_desc, ring_o, 0, tP);
-        if (elect_one()) mma_commit(dp_full);
+      if (!ok) {   // every copy has landed before the CTA may end
+        for (uint32_t k = turn > NB ? turn - NB : 0; k < turn; ++k) mbar_wait(&kv_full[k % NB], (k / NB) & 1u, quiet);
+        attn_drain(q_full, S, rq);
+        attn_drain(o_full, S, rq);
       }
-      for (int i = 0; i < n && ok; ++i) {
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA
+    constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
+    constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
+    // a resident tile (keys) times a ring tile's rows
+    auto across = [&](const uint8_t* res, uint32_t buf, const uint8_t* ring, uint32_t stage, uint32_t d, uint64_t* bar) {
+      const uint64_t a = sdesc_sw128(smem_u32(res), 16, 1024) + buf * (C::kTileBytes >> 4);
+      const uint64_t b = sdesc_sw128(smem_u32(ring), 16, 1024) + stage * (C::kTileBytes >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
+          mma_bf16(d, a + off, b + off, kIdS, kk > 0);
+        }
+        mma_commit(bar);
+      }
+    };
+    // tensor memory (keys x queries) times a ring tile, which is free afterwards
+    auto along = [&](uint32_t a, uint64_t* ready, uint32_t parity, const uint8_t* ring, uint32_t stage, uint32_t d,
+                     bool fresh, uint64_t* bar) {
+      const uint64_t b = sdesc_sw128(smem_u32(ring), T * 128, 1024) + stage * (C::kTileBytes >> 4);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (!mbar_wait_warp(&ready[c], parity, ctl)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < T / 32; ++k) {
+            const int kk = attn_part_step<32>(c, k);
+            mma_bf16_ta(d, a + attn_step_column<32>(kk), b + kk * (2048 >> 4), kIdO, !fresh || c + k > 0);
+          }
+          if (c == 1) mma_commit(bar);
+        }
+      }
+      return true;
+    };
+    RingPos r;
+    uint32_t turn = 0, step = 0;
+    while (ok && items.advance()) {
+      if (items.behind()) continue;
+      const int n = (items.t.end - first_of() + T - 1) / T * group;
+      const uint32_t buf = turn % NB;
+      ok = mbar_wait_warp(&kv_full[buf], (turn / NB) & 1u, ctl) && mbar_wait_warp(&q_full[r.stage], r.phase, ctl);
+      if (!ok) break;
+      tc_fence_after();
+      across(sk, buf, ring_q, r.stage, tS, s_full);
+      ok = mbar_wait_warp(&o_full[r.stage], r.phase, ctl);
+      if (!ok) break;
+      tc_fence_after();
+      across(sv, buf, ring_o, r.stage, tP, dp_full);
+      if (n == 1 && elect_one()) mma_commit(&kv_empty[buf]);
+      // the accumulators of the item before have been read
+      ok = mbar_wait_warp(acc_empty, (turn & 1u) ^ 1u, ctl);
+      for (int i = 0; i < n && ok; ++i, ++step) {
         RingPos nx = r;
         nx.next(S);
-        ok = along(tS, p_full, i & 1, ring_o, r.stage, tV, i == 0);
+        ok = along(tS, p_full, step & 1u, ring_o, r.stage, tV, i == 0, &o_empty[r.stage]);
         if (!ok) break;
-        if (elect_one()) mma_commit(&o_empty[r.stage]);
         if (i + 1 < n) {
           ok = mbar_wait_warp(&q_full[nx.stage], nx.phase, ctl);
           if (!ok) break;
           tc_fence_after();
-          across(k_desc, ring_q, nx.stage, tS);
-          if (elect_one()) mma_commit(s_full);
+          across(sk, buf, ring_q, nx.stage, tS, s_full);
         }
-        ok = along(tP, ds_full, i & 1, ring_q, r.stage, tK, i == 0);
+        ok = along(tP, ds_full, step & 1u, ring_q, r.stage, tK, i == 0, &q_empty[r.stage]);
         if (!ok) break;
-        if (elect_one()) mma_commit(&q_empty[r.stage]);
         if (i + 1 < n) {
           ok = mbar_wait_warp(&o_full[nx.stage], nx.phase, ctl);
           if (!ok) break;
           tc_fence_after();
-          across(v_desc, ring_o, nx.stage, tP);
-          if (elect_one()) mma_commit(dp_full);
+          across(sv, buf, ring_o, nx.stage, tP, dp_full);
+          if (i + 2 == n && elect_one()) mma_commit(&kv_empty[buf]);
         }
         r = nx;
       }
-      if (elect_one()) mma_commit(mma_done);
-      mbar_wait_warp(mma_done, 0, quiet);
-    } else if (warp == 2) {
-      // -------------------------------------------------------------- row statistics
-      // Rows past the document: lse = infinity makes their p zero.
-      RingPos r;
-      bool ok = true;
+      if (ok && elect_one()) mma_commit(acc_full);
+      ++turn;
+    }
+    if (elect_one()) mma_commit(mma_done);
+    mbar_wait_warp(mma_done, 0, quiet);
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- row statistics
+    // Rows past the document: lse = infinity makes their p zero.
+    RingPos r;
+    while (ok && items.advance()) {
+      if (items.behind()) continue;
+      const AttnTileRef t = items.t;
+      const int first = first_of(), n = (t.end - first + T - 1) / T * group;
+      int h = items.h * group, row = first;
       for (int i = 0; i < n && ok; ++i) {
-        const int h = hk * group + i / n_tiles, row = first + (i % n_tiles) * T;
         const float* a = p.stat + static_cast<size_t>(h) * p.M;
         const float* b = a + static_cast<size_t>(p.heads) * p.M;
         float l[4], d[4];
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
           l[e] = m < t.end ? a[m] : INFINITY;
           d[e] = m < t.end ? b[m] : 0.0f;
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(&st_empty[r.stage], r.phase ^ 1u, ctl));
+        ok = mbar_wait_warp(&st_empty[r.stage], r.phase ^ 1u, ctl);
         if (!ok) break;
         float* s = stat + r.stage * 2 * T;
 #pragma unroll
@@ -298,115 +301,141 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&st_full[r.stage]);
         r.next(S);
-      }
-    } else {
-      // -------------------------------------------------------------- trimming
-      // Rows past the document in its last query tile become zero: their p
-      // and ds are zero, but zero times an infinity or NaN there would not be.
-      RingPos r;
-      uint32_t landed = 0;             // a bit a stage: parity of its next landing
-      bool ok = (t.end - first) % T != 0;
-      for (int i = 0; i < n && ok; ++i) {
-        const int row = first + (i % n_tiles) * T;
-        if (row + T > t.end) {
-          for (int k = 0; k < 2 && ok; ++k) {
-            ok = __all_sync(0xffffffffu, mbar_wait(k == 0 ? &q_land[r.stage] : &o_land[r.stage],
-                                                   (landed >> r.stage) & 1u, ctl));
-            if (!ok) break;
-            attn_trim_tile<C::kBoxes>((k == 0 ? ring_q : ring_o) + r.stage * C::kTileBytes, t.end - row, lane);
-            if (lane == 0) mbar_arrive(k == 0 ? &q_full[r.stage] : &o_full[r.stage]);
-          }
-          landed ^= 1u << r.stage;
-        }
-        r.next(S);
+        row += T;
+        if (row >= t.end) { row = first; ++h; }
       }
     }
-  } else if (live && !behind) {
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------- trimming
+    // Rows past the document in its last query tile become zero: their p and
+    // ds are zero, but zero times an infinity or NaN there would not be.
+    uint32_t slot = 0, landed = 0;     // ring slots so far; a bit a stage: parity of its next landing
+    while (ok && items.advance()) {
+      if (items.behind()) continue;
+      const AttnTileRef t = items.t;
+      const int first = first_of(), n_tiles = (t.end - first + T - 1) / T;
+      const int keep = (t.end - first) % T;
+      for (int g = 0; g < group && ok && keep != 0; ++g) {
+        const uint32_t stage = (slot + n_tiles * (g + 1) - 1) % S;
+        for (int k = 0; k < 2 && ok; ++k) {
+          ok = mbar_wait_warp(k == 0 ? &q_land[stage] : &o_land[stage], (landed >> stage) & 1u, ctl);
+          if (!ok) break;
+          attn_trim_tile<C::kBoxes>((k == 0 ? ring_q : ring_o) + stage * C::kTileBytes, keep, lane);
+          if (lane == 0) mbar_arrive(k == 0 ? &q_full[stage] : &o_full[stage]);
+        }
+        landed ^= 1u << stage;
+      }
+      slot += n_tiles * group;
+    }
+  } else {
     // ---------------------------------------------------------------- elementwise
-    regs_raise<kAttnBwdRegsHigh>();
-    const int half = (warp - 4) >> 2;
+    const int quarter = (warp - 4) >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int key = t.row0 + (warp & 3) * 32 + lane;
-    const uint32_t rS = tS + lanes + 64 * half, rP = tP + lanes + 64 * half;
-    const bool all_keys = min(t.row0 + T, t.end) <= t.prefix_end;
+    const uint32_t rS = tS + lanes + 32 * quarter, rP = tP + lanes + 32 * quarter;
     RingPos r;
-    bool ok = true;
-    for (int i = 0; i < n && ok; ++i) {
-      const AttnScore<kCap, kBias> score(p, hk * group + i / n_tiles);
-      const int i0 = first + (i % n_tiles) * T + 64 * half;          // the first of this thread's 64 queries
-      ok = mbar_wait(&st_full[r.stage], r.phase, ctl) && mbar_wait(s_full, i & 1, ctl);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const float* st = stat + r.stage * 2 * T + 64 * half;
-      uint32_t v[2][32];
-      float2 g[32];                     // p, then p d(cap tanh)
-      attn_ld64(rS, v);
-      score.template apply<2, true, true>(v, i0 - key, g);
-      const float2 mul = both(score.mul);
-      const bool part = !all_keys && i0 - 64 * half < t.row0 + T;
-      const int lim = key < t.prefix_end ? 0 : key - i0;             // queries from this one on see the key
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(st + 32 * c + e);
-          const float2 nl[2] = {make_float2(-l.x, -l.y), make_float2(-l.z, -l.w)};
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int i = 16 * c + e / 2 + u;
-            const float2 y = attn_exp2<kAttnBwdPoly>(fma2(pair_of(&v[c][e + 2 * u]), mul, nl[u]), i);
-            AttnScore<kCap, kBias>::put(v[c], e + 2 * u, y);
-          }
-        }
-        if (part) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (32 * c + e < lim) v[c][e] = 0u;
-        }
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float2 y = pair_of(&v[c][e]);
-          w[e / 2] = pack_bf16x2(y.x, y.y);
-          g[16 * c + e / 2] = kCap ? mul2(y, g[16 * c + e / 2]) : y;
-        }
-        tmem_st16(rS + 16 * c, w);
-        attn_publish(&p_full[c], lane);
+    uint32_t turn = 0, step = 0;
+    while (ok && items.advance()) {
+      const AttnTileRef t = items.t;
+      const int hk = items.h;
+      if (items.behind()) {
+        const int last = min(t.row0 + T, t.end);
+        attn_zero_rows<D>(p.dK, p.kv_heads, hk, t.row0, last, threadIdx.x - 128, 512);
+        attn_zero_rows<D>(p.dV, p.kv_heads, hk, t.row0, last, threadIdx.x - 128, 512);
+        continue;
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(dp_full, i & 1, ctl));
-      if (!ok) break;
-      tc_fence_after();
-      attn_ld64(rP, v);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 d = *reinterpret_cast<const float4*>(st + T + 32 * c + e);
-          const float2 a = mul2(g[16 * c + e / 2], add2(pair_of(&v[c][e]), make_float2(-d.x, -d.y)));
-          const float2 b = mul2(g[16 * c + e / 2 + 1], add2(pair_of(&v[c][e + 2]), make_float2(-d.z, -d.w)));
-          w[e / 2] = pack_bf16x2(a.x, a.y);
-          w[e / 2 + 1] = pack_bf16x2(b.x, b.y);
-        }
-        tmem_st16(rP + 16 * c, w);
-        attn_publish(&ds_full[c], lane);
-      }
-      if (lane == 0) mbar_arrive(&st_empty[r.stage]);
-      r.next(S);
-    }
-    // the first warpgroup stores dk, the second dv
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(mma_done, 0, ctl));
-    if (ok) {
-      tc_fence_after();
-      __nv_bfloat16* out = (half == 0 ? p.dK : p.dV) + (static_cast<size_t>(key) * p.kv_heads + hk) * D;
-      const float by = half == 0 ? p.scale : 1.0f;
-#pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        tmem_ld32((half == 0 ? tK : tV) + lanes + c, o);
+      const int first = first_of(), n = (t.end - first + T - 1) / T * group;
+      const int key = t.row0 + (warp & 3) * 32 + lane;
+      const bool all_keys = min(t.row0 + T, t.end) <= t.prefix_end;
+      int h = hk * group, tile0 = first;
+      for (int i = 0; i < n && ok; ++i, ++step) {
+        const AttnScore<kCap, kBias> score(p, h);
+        const int i0 = tile0 + 32 * quarter;                           // the first of this thread's 32 queries
+        ok = mbar_wait_warp(&st_full[r.stage], r.phase, ctl) && mbar_wait_warp(s_full, step & 1u, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        const float* st = stat + r.stage * 2 * T + 32 * quarter;
+        uint32_t v[1][32];
+        float2 g[16];                     // p, then p d(cap tanh)
+        tmem_ld32(rS, v[0]);
         tmem_wait_ld();
-        if (key < t.end) attn_store32(out + c, o, by);
+        score.template apply<1, true, true>(v, i0 - key, g);
+        const float2 mul = both(score.mul);
+        const bool part = !all_keys && tile0 < t.row0 + T;
+        const int lim = key < t.prefix_end ? 0 : key - i0;             // queries from this one on see the key
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 16 * c; e < 16 * c + 16; e += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(st + e);
+            const float2 nl[2] = {make_float2(-l.x, -l.y), make_float2(-l.z, -l.w)};
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              AttnScore<kCap, kBias>::put(v[0], e + 2 * u,
+                                          attn_exp2<kAttnBwdPoly>(fma2(pair_of(&v[0][e + 2 * u]), mul, nl[u]), e / 2 + u));
+          }
+          if (part) {
+#pragma unroll
+            for (int e = 16 * c; e < 16 * c + 16; ++e)
+              if (e < lim) v[0][e] = 0u;
+          }
+#pragma unroll
+          for (int e = 16 * c; e < 16 * c + 16; e += 2) {
+            const float2 y = pair_of(&v[0][e]);
+            w[e / 2 - 8 * c] = pack_bf16x2(y.x, y.y);
+            g[e / 2] = kCap ? mul2(y, g[e / 2]) : y;
+          }
+          tmem_st8(rS + 8 * c, w);
+          attn_publish(&p_full[c], lane);
+        }
+        ok = mbar_wait_warp(dp_full, step & 1u, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        tmem_ld32(rP, v[0]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 16 * c; e < 16 * c + 16; e += 4) {
+            const float4 d = *reinterpret_cast<const float4*>(st + T + e);
+            const float2 a = mul2(g[e / 2], add2(pair_of(&v[0][e]), make_float2(-d.x, -d.y)));
+            const float2 b = mul2(g[e / 2 + 1], add2(pair_of(&v[0][e + 2]), make_float2(-d.z, -d.w)));
+            w[e / 2 - 8 * c] = pack_bf16x2(a.x, a.y);
+            w[e / 2 - 8 * c + 1] = pack_bf16x2(b.x, b.y);
+          }
+          tmem_st8(rP + 8 * c, w);
+          attn_publish(&ds_full[c], lane);
+        }
+        if (lane == 0) mbar_arrive(&st_empty[r.stage]);
+        r.next(S);
+        tile0 += T;
+        if (tile0 >= t.end) { tile0 = first; ++h; }
+      }
+      ok = ok && mbar_wait_warp(acc_full, turn & 1u, ctl);
+      if (!ok) break;
+      ++turn;
+      tc_fence_after();
+      // half of the warps store dk, half dv
+      const bool is_k = quarter < 2;
+      const int f0 = (quarter & 1) * (D / 2);
+      const float by = is_k ? p.scale : 1.0f;
+      uint4 w[D / 16];
+#pragma unroll
+      for (int c = 0; c < D / 2; c += 32) {
+        uint32_t o[32];
+        tmem_ld32((is_k ? tK : tV) + lanes + f0 + c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) w[(c + e) / 8] = attn_pack8(&o[e], by);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty);
+      if (key < t.end) {
+        uint4* out = reinterpret_cast<uint4*>((is_k ? p.dK : p.dV) + (static_cast<size_t>(key) * p.kv_heads + hk) * D + f0);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) out[k] = w[k];
       }
     }
   }
@@ -432,7 +461,7 @@ struct AttnDqCfg {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = kAttnTile * D * 2;
   static constexpr int kStagesK = D == 128 ? 3 : 4, kStagesV = D == 128 ? 2 : 4;
-  static constexpr int kBars = 2 * kStagesK + 2 * kStagesV + 1 + 1 + 2 + 1 + 1 + 1;
+  static constexpr int kBars = 3 * kStagesK + 3 * kStagesV + 2 + 2 + 1 + 1 + 2 + 1;
   static constexpr int kSmemBytes = (2 + kStagesK + kStagesV) * kTileBytes + kBars * 8 + 16 + 1024;
   static_assert(kSmemBytes <= kSmemLimitBytes, "shared memory");
 };
@@ -452,12 +481,16 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
   uint64_t* k_empty = k_full + SK;
   uint64_t* v_full = k_empty + SK;
   uint64_t* v_empty = v_full + SV;
-  uint64_t* qo_full = v_empty + SV;
-  uint64_t* land = qo_full + 1;
-  uint64_t* s_full = land + 1;         // [2]
+  uint64_t* k_land = v_empty + SV;     // tiles that are trimmed before they count as full
+  uint64_t* v_land = k_land + SK;
+  uint64_t* qo_full = v_land + SV;
+  uint64_t* qo_empty = qo_full + 1;
+  uint64_t* s_full = qo_empty + 1;     // [2]
   uint64_t* dp_full = s_full + 2;
   uint64_t* ds_full = dp_full + 1;
-  uint64_t* mma_done = ds_full + 1;
+  uint64_t* acc_full = ds_full + 1;    // dq of the item is complete
+  uint64_t* acc_empty = acc_full + 1;  // ... and has been read
+  uint64_t* mma_done = acc_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   AbortCtl ctl{abort_flag, p.plan.head};
@@ -466,14 +499,16 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < SK; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
-    for (int i = 0; i < SV; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1); }
+    for (int i = 0; i < SK; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); mbar_init(&k_land[i], 1); }
+    for (int i = 0; i < SV; ++i) { mbar_init(&v_full[i], 1); mbar_init(&v_empty[i], 1); mbar_init(&v_land[i], 1); }
     mbar_init(qo_full, 1);
-    mbar_init(land, 1);
+    mbar_init(qo_empty, 1);
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 16);
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, 8);
+    mbar_init(ds_full, 16);
     mbar_init(mma_done, 1);
     *abort_flag = 0u;
     fence_mbar_init();
@@ -486,182 +521,222 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
   const uint32_t tQ = tbase, tP = tbase + 128, tS = tbase + 256;
   grid_dep_wait();
 
-  const uint32_t tile = blockIdx.x / static_cast<uint32_t>(p.heads);
-  const int h = static_cast<int>(blockIdx.x - tile * static_cast<uint32_t>(p.heads));
-  const bool live = attn_plan_ok(p) && tile < p.plan.head[kPlanQ];
-  AttnTileRef t{0, 0, 0, 0};
-  if (live) t = p.plan.q[tile];
-  const bool behind = t.prefix_end < 0;
-  if (behind) attn_zero_rows<D>(p.dQ, p.heads, h, t.row0, min(t.row0 + T, t.end));
-  const int hk = h / (p.heads / p.kv_heads);
-  const int n = attn_key_tiles(t, t.row0, T);
+  AttnItems items(p.plan.q, attn_plan_ok(p) ? p.plan.head[kPlanQ] : 0u, p.heads);
+  const int group = p.heads / p.kv_heads;
+  bool ok = true;
 
-  if (live && !behind && warp < 4) {
-    regs_lower<kAttnBwdRegsLow>();
-    if (warp == 0) {
-      // -------------------------------------------------------------- TMA
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA
+    if (lane == 0) {
       RingPos rk, rv;
-      uint32_t landed = 0;
-      bool ok = true;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(qo_full, 2 * C::kTileBytes);
-        for (int b = 0; b < C::kBoxes; ++b) {
-          tma_load_2d(sq + b * (T * 128), &maps.q, qo_full, h * D + 64 * b, t.row0);
-          tma_load_2d(so + b * (T * 128), &maps.d_o, qo_full, h * D + 64 * b, t.row0);
-        }
-      }
-      for (int j = 0; j < n && ok; ++j) {
-        const int row = t.begin + j * T;
-        // Rows past the document become zero (see the trimming in attn_dkv_kernel).
-        const bool trim = row + T > t.end;
-        for (int k = 0; k < 2 && ok; ++k) {
-          RingPos& r = k == 0 ? rk : rv;
-          ok = __all_sync(0xffffffffu, mbar_wait(k == 0 ? &k_empty[r.stage] : &v_empty[r.stage], r.phase ^ 1u, ctl));
-          if (!ok) break;
-          uint8_t* dst = (k == 0 ? ring_k : ring_v) + r.stage * C::kTileBytes;
-          uint64_t* full = k == 0 ? &k_full[r.stage] : &v_full[r.stage];
-          uint64_t* bar = trim ? land : full;
-          if (lane == 0) {
+      uint32_t turn = 0;
+      while (ok && items.advance()) {
+        if (items.behind()) continue;
+        const AttnTileRef t = items.t;
+        const int h = items.h, hk = h / group, n = attn_key_tiles(t, t.row0, T);
+        for (int j = 0; j < n && ok; ++j) {
+          const int row = t.begin + j * T;
+          const bool trim = row + T > t.end;     // rows past the document become zero, as in attn_dkv_kernel
+          for (int k = 0; k < 2 && ok; ++k) {
+            RingPos& r = k == 0 ? rk : rv;
+            ok = mbar_wait(k == 0 ? &k_empty[r.stage] : &v_empty[r.stage], r.phase ^ 1u, ctl);
+            if (!ok) break;
+            uint8_t* dst = (k == 0 ? ring_k : ring_v) + r.stage * C::kTileBytes;
+            uint64_t* bar = k == 0 ? (trim ? &k_land[r.stage] : &k_full[r.stage])
+                                   : (trim ? &v_land[r.stage] : &v_full[r.stage]);
             mbar_arrive_expect_tx(bar, C::kTileBytes);
             for (int b = 0; b < C::kBoxes; ++b)
               tma_load_2d(dst + b * (T * 128), k == 0 ? &maps.k : &maps.v, bar, hk * D + 64 * b, row);
+            r.next(k == 0 ? SK : SV);
+            if (j == 0 && k == 0) {
+              ok = mbar_wait(qo_empty, (turn & 1u) ^ 1u, ctl);
+              if (!ok) break;
+              ++turn;
+              mbar_arrive_expect_tx(qo_full, 2 * C::kTileBytes);
+              for (int b = 0; b < C::kBoxes; ++b) {
+                tma_load_2d(sq + b * (T * 128), &maps.q, qo_full, h * D + 64 * b, t.row0);
+                tma_load_2d(so + b * (T * 128), &maps.d_o, qo_full, h * D + 64 * b, t.row0);
+              }
+            }
           }
-          if (trim) {
-            ok = __all_sync(0xffffffffu, mbar_wait(land, landed & 1u, quiet));
-            ++landed;
-            attn_trim_tile<C::kBoxes>(dst, t.end - row, lane);
-            if (lane == 0) mbar_arrive(full);
-          }
-          r.next(k == 0 ? SK : SV);
         }
       }
-      if (lane == 0 && !ok) {
-        mbar_wait(qo_full, 0, quiet);
+      if (!ok) {   // every copy has landed before the CTA may end
+        mbar_wait(qo_full, (turn & 1u) ^ 1u, quiet);
         attn_drain(k_full, SK, rk);
         attn_drain(v_full, SV, rv);
       }
-    } else if (warp == 1) {
-      // -------------------------------------------------------------- MMA
-      constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
-      constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
-      auto across = [&](const uint8_t* a, const uint8_t* ring, uint32_t stage, uint32_t d) {
-        const uint64_t ad = sdesc_sw128(smem_u32(a), 16, 1024);
-        const uint64_t b = sdesc_sw128(smem_u32(ring), 16, 1024) + stage * (C::kTileBytes >> 4);
-        if (elect_one()) {
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA
+    constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
+    constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
+    auto across = [&](const uint8_t* res, const uint8_t* ring, uint32_t stage, uint32_t d, uint64_t* bar, uint64_t* bar2) {
+      const uint64_t a = sdesc_sw128(smem_u32(res), 16, 1024);
+      const uint64_t b = sdesc_sw128(smem_u32(ring), 16, 1024) + stage * (C::kTileBytes >> 4);
+      if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
-            mma_bf16(d, ad + off, b + off, kIdS, kk > 0);
-          }
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
+          mma_bf16(d, a + off, b + off, kIdS, kk > 0);
         }
-      };
-      RingPos ks, kd, v;             // K tiles of the scores, of dQ; V tiles
-      auto scores = [&](int j) {
-        if (!mbar_wait_warp(&k_full[ks.stage], ks.phase, ctl)) return false;
-        tc_fence_after();
-        across(sq, ring_k, ks.stage, tS + (j & 1) * T);
-        if (elect_one()) mma_commit(&s_full[j & 1]);
-        ks.next(SK);
-        return true;
-      };
-      auto values = [&]() {
-        if (!mbar_wait_warp(&v_full[v.stage], v.phase, ctl)) return false;
-        tc_fence_after();
-        across(so, ring_v, v.stage, tP);
-        if (elect_one()) mma_commit(dp_full);
-        if (elect_one()) mma_commit(&v_empty[v.stage]);
-        v.next(SV);
-        return true;
-      };
-      bool ok = mbar_wait_warp(qo_full, 0, ctl);
-      ok = ok && scores(0) && values();
-      if (n > 1) ok = ok && scores(1);
-      for (int j = 0; j < n && ok; ++j) {
-        ok = mbar_wait_warp(ds_full, j & 1, ctl);
+        mma_commit(bar);
+        if (bar2 != nullptr) mma_commit(bar2);
+      }
+    };
+    RingPos ks, kd, v;             // K tiles of the scores, of dQ; V tiles
+    uint32_t turn = 0, issued = 0, step = 0;      // items; score tiles issued; dS tiles taken
+    auto scores = [&]() {
+      if (!mbar_wait_warp(&k_full[ks.stage], ks.phase, ctl)) return false;
+      tc_fence_after();
+      across(sq, ring_k, ks.stage, tS + (issued & 1u) * T, &s_full[issued & 1u], nullptr);
+      ++issued;
+      ks.next(SK);
+      return true;
+    };
+    auto values = [&]() {
+      if (!mbar_wait_warp(&v_full[v.stage], v.phase, ctl)) return false;
+      tc_fence_after();
+      across(so, ring_v, v.stage, tP, dp_full, &v_empty[v.stage]);
+      v.next(SV);
+      return true;
+    };
+    while (ok && items.advance()) {
+      if (items.behind()) continue;
+      const int n = attn_key_tiles(items.t, items.t.row0, T);
+      ok = mbar_wait_warp(qo_full, turn & 1u, ctl);
+      ok = ok && scores() && values();
+      if (n > 1) ok = ok && scores();
+      if (ok && n == 1 && elect_one()) mma_commit(qo_empty);
+      // the accumulator of the item before has been read
+      ok = ok && mbar_wait_warp(acc_empty, (turn & 1u) ^ 1u, ctl);
+      for (int j = 0; j < n && ok; ++j, ++step) {
+        ok = mbar_wait_warp(ds_full, step & 1u, ctl);
         if (!ok) break;
         tc_fence_after();
-        if (j + 1 < n) ok = values();
-        if (!ok) break;
+        if (j + 1 < n) {
+          ok = values();
+          if (!ok) break;
+          if (j + 2 == n && elect_one()) mma_commit(qo_empty);       // the last use of Q and dO
+        }
         const uint64_t b = sdesc_sw128(smem_u32(ring_k), T * 128, 1024) + kd.stage * (C::kTileBytes >> 4);
-        const uint32_t a = tS + (j & 1) * T;
+        const uint32_t a = tS + (step & 1u) * T;
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < T / 16; ++kk)
-            mma_bf16_ta(tQ, a + attn_step_column(kk), b + kk * (2048 >> 4), kIdO, j > 0 || kk > 0);
+            mma_bf16_ta(tQ, a + attn_step_column<32>(kk), b + kk * (2048 >> 4), kIdO, j > 0 || kk > 0);
+          mma_commit(&k_empty[kd.stage]);
         }
-        if (elect_one()) mma_commit(&k_empty[kd.stage]);
         kd.next(SK);
-        if (j + 2 < n) ok = scores(j + 2);
+        if (j + 2 < n) ok = scores();
       }
-      if (elect_one()) mma_commit(mma_done);
-      mbar_wait_warp(mma_done, 0, quiet);
+      if (ok && elect_one()) mma_commit(acc_full);
+      ++turn;
     }
-  } else if (live && !behind) {
+    if (elect_one()) mma_commit(mma_done);
+    mbar_wait_warp(mma_done, 0, quiet);
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- trimming
+    uint32_t slot = 0, k_landed = 0, v_landed = 0;
+    while (ok && items.advance()) {
+      if (items.behind()) continue;
+      const AttnTileRef t = items.t;
+      const int n = attn_key_tiles(t, t.row0, T), row = t.begin + (n - 1) * T;
+      slot += n;
+      if (row + T > t.end) {
+        const uint32_t sk = (slot - 1) % SK, sv = (slot - 1) % SV;
+        ok = mbar_wait_warp(&k_land[sk], (k_landed >> sk) & 1u, ctl);
+        if (!ok) break;
+        attn_trim_tile<C::kBoxes>(ring_k + sk * C::kTileBytes, t.end - row, lane);
+        if (lane == 0) mbar_arrive(&k_full[sk]);
+        ok = mbar_wait_warp(&v_land[sv], (v_landed >> sv) & 1u, ctl);
+        if (!ok) break;
+        attn_trim_tile<C::kBoxes>(ring_v + sv * C::kTileBytes, t.end - row, lane);
+        if (lane == 0) mbar_arrive(&v_full[sv]);
+        k_landed ^= 1u << sk;
+        v_landed ^= 1u << sv;
+      }
+    }
+  } else if (warp >= 4) {
     // ---------------------------------------------------------------- elementwise
-    regs_raise<kAttnBwdRegsHigh>();
-    const int half = (warp - 4) >> 2;
+    const int quarter = (warp - 4) >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int row = t.row0 + (warp & 3) * 32 + lane;
-    const bool mine = row < t.end;
-    const int see = min(max(row + 1, t.prefix_end), t.end);              // keys [begin, see)
-    const int all = min(max(t.row0 + 1, t.prefix_end), t.end);           // ... that every row sees
-    const float lse2 = mine ? p.stat[static_cast<size_t>(h) * p.M + row] : INFINITY;
-    const float delta = mine ? p.stat[static_cast<size_t>(p.heads + h) * p.M + row] : 0.0f;
-    const AttnScore<kCap, kBias> score(p, h);
-    const float2 mul = both(score.mul), shift = both(-lse2);
-    bool ok = true;
-    for (int j = 0; j < n && ok; ++j) {
-      const int j0 = t.begin + j * T + 64 * half;                        // the first of this thread's 64 keys
-      const uint32_t rS = tS + (j & 1) * T + lanes + 64 * half, rP = tP + lanes + 64 * half;
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[j & 1], (j >> 1) & 1, ctl));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t v[2][32];
-      float2 g[32];                     // p d(cap tanh)
-      attn_ld64(rS, v);
-      score.template apply<2, true, true>(v, j0 - row, g);
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
+    const uint32_t rP = tP + lanes + 32 * quarter;
+    uint32_t turn = 0, step = 0;
+    while (ok && items.advance()) {
+      const AttnTileRef t = items.t;
+      const int h = items.h;
+      if (items.behind()) {
+        attn_zero_rows<D>(p.dQ, p.heads, h, t.row0, min(t.row0 + T, t.end), threadIdx.x - 128, 512);
+        continue;
+      }
+      const int n = attn_key_tiles(t, t.row0, T);
+      const int row = t.row0 + (warp & 3) * 32 + lane;
+      const bool mine = row < t.end;
+      const int see = min(max(row + 1, t.prefix_end), t.end);              // keys [begin, see)
+      const int all = min(max(t.row0 + 1, t.prefix_end), t.end);           // ... that every row sees
+      const float lse2 = mine ? p.stat[static_cast<size_t>(h) * p.M + row] : INFINITY;
+      const float delta = mine ? p.stat[static_cast<size_t>(p.heads + h) * p.M + row] : 0.0f;
+      const AttnScore<kCap, kBias> score(p, h);
+      const float2 mul = both(score.mul), shift = both(-lse2);
+      for (int j = 0; j < n && ok; ++j, ++step) {
+        const int j0 = t.begin + j * T + 32 * quarter;                     // the first of this thread's 32 keys
+        const uint32_t rS = tS + (step & 1u) * T + lanes + 32 * quarter;
+        ok = mbar_wait_warp(&s_full[step & 1u], (step >> 1) & 1u, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t v[1][32];
+        float2 g[16];                     // p d(cap tanh)
+        tmem_ld32(rS, v[0]);
+        tmem_wait_ld();
+        score.template apply<1, true, true>(v, j0 - row, g);
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const int i = 16 * c + e / 2;
-          const float2 y = attn_exp2<kAttnBwdPoly>(fma2(pair_of(&v[c][e]), mul, shift), i);
-          g[i] = kCap ? mul2(y, g[i]) : y;
+          const float2 y = attn_exp2<kAttnBwdPoly>(fma2(pair_of(&v[0][e]), mul, shift), e / 2);
+          g[e / 2] = kCap ? mul2(y, g[e / 2]) : y;
         }
-      if (j0 + 64 > all) {
-        const int lim = see - j0;
+        if (j0 + 32 > all) {
+          const int lim = see - j0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (2 * i >= lim) g[i].x = 0.0f;
-          if (2 * i + 1 >= lim) g[i].y = 0.0f;
+          for (int i = 0; i < 16; ++i) {
+            if (2 * i >= lim) g[i].x = 0.0f;
+            if (2 * i + 1 >= lim) g[i].y = 0.0f;
+          }
         }
-      }
-      ok = __all_sync(0xffffffffu, mbar_wait(dp_full, j & 1, ctl));
-      if (!ok) break;
-      tc_fence_after();
-      attn_ld64(rP, v);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
+        ok = mbar_wait_warp(dp_full, step & 1u, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        tmem_ld32(rP, v[0]);
+        tmem_wait_ld();
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float2 y = mul2(g[16 * c + e / 2], add2(pair_of(&v[c][e]), both(-delta)));
+          const float2 y = mul2(g[e / 2], add2(pair_of(&v[0][e]), both(-delta)));
           w[e / 2] = pack_bf16x2(y.x, y.y);
         }
-        tmem_st16(rS + 16 * c, w);
+        tmem_st16(rS, w);
+        attn_publish(ds_full, lane);
       }
-      attn_publish(ds_full, lane);
-    }
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(mma_done, 0, ctl));
-    if (ok) {
+      ok = ok && mbar_wait_warp(acc_full, turn & 1u, ctl);
+      if (!ok) break;
+      ++turn;
       tc_fence_after();
-      __nv_bfloat16* out = p.dQ + (static_cast<size_t>(row) * p.heads + h) * D + half * (D / 2);
+      uint4 w[D / 32];
 #pragma unroll
-      for (int c = 0; c < D / 2; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(tQ + lanes + half * (D / 2) + c, o);
+      for (int c = 0; c < D / 4; c += 16) {
+        uint32_t o[16];
+        tmem_ld16(tQ + lanes + quarter * (D / 4) + c, o);
         tmem_wait_ld();
-        if (mine) attn_store32(out + c, o, p.scale);
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) w[(c + e) / 8] = attn_pack8(&o[e], p.scale);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty);
+      if (mine) {
+        uint4* out = reinterpret_cast<uint4*>(p.dQ + (static_cast<size_t>(row) * p.heads + h) * D + quarter * (D / 4));
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) out[k] = w[k];
       }
     }
   }

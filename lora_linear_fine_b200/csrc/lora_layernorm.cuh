@@ -65,21 +65,6 @@ __device__ __forceinline__ void ln_unpack8(uint4 w, float2 (&f)[4]) {
   f[0] = unpack_bf16x2(w.x); f[1] = unpack_bf16x2(w.y); f[2] = unpack_bf16x2(w.z); f[3] = unpack_bf16x2(w.w);
 }
 
-// Whether all threads of a group say so.
-template <int T>
-__device__ __forceinline__ bool ln_group_all(bool ok, int group) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(ok)), "r"(group + 1), "n"(T)
-      : "memory");
-  return r != 0u;
-}
-
 // CTAs an SM: as many as the registers of a row in hand and the next one allow.
 template <int T>
 __global__ void __launch_bounds__(LnCfg<T>::kThreads, LnCfg<T>::kPerSm)
@@ -246,7 +231,7 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1)
     const long long row0 = blk * sh.rows;
     const int n = static_cast<int>(M - row0 < sh.rows ? M - row0 : sh.rows);
     ok = __all_sync(0xffffffffu, mbar_wait(&full[r.stage], r.phase, ctl));
-    if constexpr (T > 32) ok = ln_group_all<T>(ok, group);          // a group leaves the loop together
+    if constexpr (T > 32) ok = bar_sync_and<T>(group + 1, ok);          // a group leaves the loop together
     if (!ok) break;
     if (threadIdx.x == 0 && at > 0) fill(at - 1 + sh.stages);
     ++at;

@@ -2308,7 +2308,7 @@ bool attn_tm(CUtensorMap* tm, const void* ptr, const AttnParams& p, int heads, i
 }
 
 template <int D, bool kCap, bool kBias>
-lora_status_t launch_attn_fwd(const AttnParams& p, cudaStream_t st) {
+lora_status_t launch_attn_fwd(const AttnParams& p, int sms, cudaStream_t st) {
   AttnFwdMaps maps;
   if (!attn_tm(&maps.q, p.Q, p, p.heads, D) || !attn_tm(&maps.k, p.K, p, p.kv_heads, D) ||
       !attn_tm(&maps.v, p.V, p, p.kv_heads, D))
@@ -2317,45 +2317,45 @@ lora_status_t launch_attn_fwd(const AttnParams& p, cudaStream_t st) {
   LORA_TRY(kernel_ready<k>(AttnFwdCfg<D>::kSmemBytes, kAttnFwdThreads, 128 * (kAttnFwdRegsLow + 2 * kAttnFwdRegsHigh)));
   const int64_t ctas = static_cast<int64_t>(p.plan.max_fwd) * p.heads;
   if (ctas > (int64_t(1) << 31) - 1) return LORA_ERR_UNSUPPORTED;
-  launch_k(k, dim3(static_cast<unsigned>(ctas)), dim3(kAttnFwdThreads), AttnFwdCfg<D>::kSmemBytes, st, false, p, maps);
+  launch_k(k, dim3(static_cast<unsigned>(std::min<int64_t>(ctas, sms))), dim3(kAttnFwdThreads), AttnFwdCfg<D>::kSmemBytes, st, false, p, maps);
   return check_launch("attn_fwd_kernel");
 }
 
 template <int D>
-lora_status_t launch_attn_fwd_mod(const AttnParams& p, cudaStream_t st) {
+lora_status_t launch_attn_fwd_mod(const AttnParams& p, int sms, cudaStream_t st) {
   if (p.cap > 0.0f)
-    return p.slopes != nullptr ? launch_attn_fwd<D, true, true>(p, st) : launch_attn_fwd<D, true, false>(p, st);
-  return p.slopes != nullptr ? launch_attn_fwd<D, false, true>(p, st) : launch_attn_fwd<D, false, false>(p, st);
+    return p.slopes != nullptr ? launch_attn_fwd<D, true, true>(p, sms, st) : launch_attn_fwd<D, true, false>(p, sms, st);
+  return p.slopes != nullptr ? launch_attn_fwd<D, false, true>(p, sms, st) : launch_attn_fwd<D, false, false>(p, sms, st);
 }
 
 template <int D, bool kCap, bool kBias>
-lora_status_t launch_attn_bwd(const AttnParams& p, cudaStream_t st) {
+lora_status_t launch_attn_bwd(const AttnParams& p, int sms, cudaStream_t st) {
   AttnBwdMaps maps;
   if (!attn_tm(&maps.q, p.Q, p, p.heads, D) || !attn_tm(&maps.k, p.K, p, p.kv_heads, D) ||
       !attn_tm(&maps.v, p.V, p, p.kv_heads, D) || !attn_tm(&maps.d_o, p.dO, p, p.heads, D))
     return LORA_ERR_CUDA;
   constexpr auto kv = attn_dkv_kernel<D, kCap, kBias>;
   constexpr auto q = attn_dq_kernel<D, kCap, kBias>;
-  constexpr int kRegs = 128 * (kAttnBwdRegsLow + 2 * kAttnBwdRegsHigh);
-  LORA_TRY(kernel_ready<kv>(AttnDkvCfg<D>::kSmemBytes, kAttnBwdThreads, kRegs));
-  LORA_TRY(kernel_ready<q>(AttnDqCfg<D>::kSmemBytes, kAttnBwdThreads, kRegs));
+  LORA_TRY(kernel_ready<kv>(AttnDkvCfg<D>::kSmemBytes));
+  LORA_TRY(kernel_ready<q>(AttnDqCfg<D>::kSmemBytes));
   const int64_t ctas = static_cast<int64_t>(p.plan.max_q) * p.heads;
   if (ctas > (int64_t(1) << 31) - 1) return LORA_ERR_UNSUPPORTED;
   launch_k(attn_delta_kernel<D>, dim3(static_cast<unsigned>(ceil_div(p.M, 32)), static_cast<unsigned>(ceil_div(p.heads, 8))),
            dim3(256), 0, st, false, p);
   LORA_TRY(check_launch("attn_delta_kernel"));
-  launch_k(kv, dim3(static_cast<unsigned>(static_cast<int64_t>(p.plan.max_q) * p.kv_heads)), dim3(kAttnBwdThreads),
-           AttnDkvCfg<D>::kSmemBytes, st, false, p, maps);
+  launch_k(kv, dim3(static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(p.plan.max_q) * p.kv_heads, sms))),
+           dim3(kAttnBwdThreads), AttnDkvCfg<D>::kSmemBytes, st, false, p, maps);
   LORA_TRY(check_launch("attn_dkv_kernel"));
-  launch_k(q, dim3(static_cast<unsigned>(ctas)), dim3(kAttnBwdThreads), AttnDqCfg<D>::kSmemBytes, st, false, p, maps);
+  launch_k(q, dim3(static_cast<unsigned>(std::min<int64_t>(ctas, sms))), dim3(kAttnBwdThreads), AttnDqCfg<D>::kSmemBytes,
+           st, false, p, maps);
   return check_launch("attn_dq_kernel");
 }
 
 template <int D>
-lora_status_t launch_attn_bwd_mod(const AttnParams& p, cudaStream_t st) {
+lora_status_t launch_attn_bwd_mod(const AttnParams& p, int sms, cudaStream_t st) {
   if (p.cap > 0.0f)
-    return p.slopes != nullptr ? launch_attn_bwd<D, true, true>(p, st) : launch_attn_bwd<D, true, false>(p, st);
-  return p.slopes != nullptr ? launch_attn_bwd<D, false, true>(p, st) : launch_attn_bwd<D, false, false>(p, st);
+    return p.slopes != nullptr ? launch_attn_bwd<D, true, true>(p, sms, st) : launch_attn_bwd<D, true, false>(p, sms, st);
+  return p.slopes != nullptr ? launch_attn_bwd<D, false, true>(p, sms, st) : launch_attn_bwd<D, false, false>(p, sms, st);
 }
 
 }  // namespace
@@ -2510,8 +2510,8 @@ lora_status_t lora_linear_attn_fwd(const lora_attn_desc* d, void* plan, size_t p
   if (d->M == 0) return LORA_OK;
   AttnParams p = attn_params(d, plan, Q, K, V, slopes, lse);
   p.O = static_cast<__nv_bfloat16*>(O);
-  return d->head_dim == 64 ? launch_attn_fwd_mod<64>(p, static_cast<cudaStream_t>(stream))
-                           : launch_attn_fwd_mod<128>(p, static_cast<cudaStream_t>(stream));
+  return d->head_dim == 64 ? launch_attn_fwd_mod<64>(p, dev.sms, static_cast<cudaStream_t>(stream))
+                           : launch_attn_fwd_mod<128>(p, dev.sms, static_cast<cudaStream_t>(stream));
 }
 
 size_t lora_linear_attn_workspace_size(const lora_attn_desc* d) {
@@ -2543,8 +2543,8 @@ lora_status_t lora_linear_attn_bwd(const lora_attn_desc* d, void* plan, size_t p
   p.dK = static_cast<__nv_bfloat16*>(dK);
   p.dV = static_cast<__nv_bfloat16*>(dV);
   p.stat = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
-  return d->head_dim == 64 ? launch_attn_bwd_mod<64>(p, static_cast<cudaStream_t>(stream))
-                           : launch_attn_bwd_mod<128>(p, static_cast<cudaStream_t>(stream));
+  return d->head_dim == 64 ? launch_attn_bwd_mod<64>(p, dev.sms, static_cast<cudaStream_t>(stream))
+                           : launch_attn_bwd_mod<128>(p, dev.sms, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
