@@ -261,47 +261,56 @@ __device__ __forceinline__ float2 attn_exp2(float2 x, int i) {
   return (i & 3) < kPoly ? exp2_poly(x) : make_float2(ex2(x.x), ex2(x.y));
 }
 
-// Scores as values whose exponent of 2 is `mul` times them: the raw products
-// (mul = scale log2(e)), with a cap the tanh (mul = cap log2(e)), with a bias
-// z log2(e) (mul = 1).
-//   tanh(y) = y P(y^2), P of degree 4 with the least largest error for
-//   |y| <= 0.6 (2^-23.7), where all of a warp's values are that small: FMAs
-//   alone.  Else tanh(y) = 1 - 2 / (1 + exp(2 y)), two special functions, right
-//   at both ends (0 and infinity in the denominator), within a few 2^-24.
+// A score's exponent of 2 is value * mul - slope2 |i - j|: the values are the
+// raw products (mul = scale log2(e)) or, with a cap, their tanh (mul = cap
+// log2(e)).
+//   tanh(y) = y P(y^2), P of degree 3 with the least largest error for
+//   |y| <= 0.4 (2^-23.3), where all of a warp's values are that small and the
+//   powers of scale / cap folded into P's coefficients are within fp32's range:
+//   FMAs alone, 5 for a pair.  Else tanh(y) = 1 - 2 / (1 + exp(2 y)), two
+//   special functions a value, right at both ends (0 and infinity in the
+//   denominator), within a few 2^-24.
 template <bool kCap, bool kBias>
 struct AttnScore {
   float mul;
-  float headroom;   // 16 / mul: how far values may outgrow the running reference
-  float pre, cap2, slope2;
-  __device__ __forceinline__ AttnScore(const AttnParams& p, int h) {
-    cap2 = kCap ? p.cap * kLog2e : 0.0f;
-    pre = kCap ? p.scale / p.cap : p.scale * kLog2e;
-    slope2 = kBias ? p.slopes[h] * kLog2e : 0.0f;
-    mul = kBias ? 1.0f : kCap ? cap2 : pre;
-    headroom = 16.0f / mul;
-  }
-  // 32 kChunks products of a row in place; dist0 = distance (either sign) of
-  // the first, rising by 1 (kUp) or falling by 1 from one to the next.
-  // dt: 1 - tanh^2 (only with a cap).
-  template <int kChunks, bool kUp, bool kWantDt>
-  __device__ __forceinline__ void apply(uint32_t (&v)[kChunks][32], int dist0, float2* dt) const {
+  float slope2 = 0.0f;
+  float pre = 0.0f, limit = 0.0f, a0 = 0.0f, a1 = 0.0f, a2 = 0.0f, a3 = 0.0f;
+  __device__ __forceinline__ explicit AttnScore(const AttnParams& p) : mul((kCap ? p.cap : p.scale) * kLog2e) {
     if constexpr (kCap) {
-      float top = 0.0f;
+      pre = p.scale / p.cap;
+      limit = pre > 0x1p-17f && pre < 0x1p16f ? 0.4f / pre : -1.0f;
+      const float u = pre * pre;
+      a0 = 0.9999998807907104f * pre;
+      a1 = -0.333313912153244f * pre * u;
+      a2 = 0.1327143758535385f * pre * u * u;
+      a3 = -0.04757281020283699f * pre * u * u * u;
+    }
+  }
+  __device__ __forceinline__ void head(const AttnParams& p, int h) {
+    if constexpr (kBias) slope2 = p.slopes[h] * kLog2e;
+  }
+  // 32 kChunks products of a row become values; dt: 1 - tanh^2 (only with a cap).
+  template <int kChunks, bool kWantDt>
+  __device__ __forceinline__ void values(uint32_t (&v)[kChunks][32], float2* dt) const {
+    if constexpr (kCap) {
+      float top[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) top = max3_abs(top, __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
-      if (!__any_sync(0xffffffffu, top * pre > 0.6f)) {
+        for (int e = 0; e < 32; e += 4) {
+          top[0] = max3_abs(top[0], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+          top[1] = max3_abs(top[1], __uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3]));
+        }
+      if (!__any_sync(0xffffffffu, fmaxf(top[0], top[1]) > limit)) {
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float2 y = mul2(pair_of(&v[c][e]), both(pre)), u = mul2(y, y);
-            float2 q = fma2(both(0.015504649840295315f), u, both(-0.052122555673122406f));
-            q = fma2(q, u, both(0.13310648500919342f));
-            q = fma2(q, u, both(-0.3333234488964081f));
-            q = fma2(q, u, both(0.9999999403953552f));
-            put(v[c], e, mul2(y, q));
+            const float2 s = pair_of(&v[c][e]), u = mul2(s, s);
+            float2 q = fma2(both(a3), u, both(a2));
+            q = fma2(q, u, both(a1));
+            q = fma2(q, u, both(a0));
+            put(v[c], e, mul2(s, q));
           }
       } else {
 #pragma unroll
@@ -317,28 +326,28 @@ struct AttnScore {
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const float2 t = pair_of(&v[c][e]);
-            dt[16 * c + e / 2] = fma2(make_float2(-t.x, -t.y), t, both(1.0f));
+            dt[16 * c + e / 2] = fma2(mul2(t, t), both(-1.0f), both(1.0f));
           }
       }
     }
-    if constexpr (kBias) {
-      const float2 d0 = both(static_cast<float>(dist0));
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          constexpr float kSign = kUp ? 1.0f : -1.0f;
-          const float2 d = add2(d0, make_float2(kSign * (32 * c + e), kSign * (32 * c + e + 1)));
-          const float2 z = mul2(pair_of(&v[c][e]), both(kCap ? cap2 : pre));
-          put(v[c], e, make_float2(fmaf(-slope2, fabsf(d.x), z.x), fmaf(-slope2, fabsf(d.y), z.y)));
-        }
-    }
+  }
+  // one product's value
+  __device__ __forceinline__ float one(float s) const {
+    return kCap ? fmaf(-2.0f, rcp_approx(1.0f + ex2(s * (2.0f * kLog2e * pre))), 1.0f) : s;
+  }
+  // `base` minus the bias at distances d0 + c and d0 + c + 1 (either sign)
+  __device__ __forceinline__ float2 shifted(float2 base, float d0, float c, float step) const {
+    if constexpr (!kBias) return base;
+    const float2 d = add2(both(d0), make_float2(c, c + step));
+    return make_float2(fmaf(-slope2, fabsf(d.x), base.x), fmaf(-slope2, fabsf(d.y), base.y));
   }
   __device__ __forceinline__ static void put(uint32_t (&v)[32], int e, float2 z) {
     v[e] = __float_as_uint(z.x);
     v[e + 1] = __float_as_uint(z.y);
   }
 };
+
+constexpr float kAttnHeadroom = 16.0f;   // exponents of 2 by which scores may outgrow the running reference
 
 // The warp's stores to tensor memory are done: tell the MMA warp.
 __device__ __forceinline__ void attn_publish(uint64_t* bar, int lane) {
@@ -403,10 +412,4 @@ __device__ __forceinline__ uint4 attn_pack8(const uint32_t* v, float by) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-template <int n>
-__device__ __forceinline__ void attn_store(__nv_bfloat16* out, const uint32_t (&v)[n], float by) {
-#pragma unroll
-  for (int e = 0; e < n; e += 8) *reinterpret_cast<uint4*>(out + e) = attn_pack8(&v[e], by);
-}
-
 }  // namespace lora

@@ -25,7 +25,7 @@ struct AttnBwdMaps {
 // ---------------------------------------------------------------------------
 // delta
 // ---------------------------------------------------------------------------
-// stat[0][h][m] = lse_mh log2(e), stat[1][h][m] = delta_mh.  A CTA takes 32
+// stat[0][h][m] = -lse_mh log2(e), stat[1][h][m] = -delta_mh.  A CTA takes 32
 // rows of 8 heads; the results pass through shared memory so that both sides
 // move whole sectors.
 template <int D>
@@ -55,8 +55,21 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
   __syncthreads();
   const int m = m0 + (threadIdx.x & 31), h = h0 + (threadIdx.x >> 5);
   if (m >= p.M || h >= p.heads) return;
-  p.stat[static_cast<size_t>(h) * p.M + m] = p.lse[static_cast<size_t>(m) * p.heads + h] * kLog2e;
-  p.stat[static_cast<size_t>(p.heads + h) * p.M + m] = s[threadIdx.x >> 5][threadIdx.x & 31];
+  p.stat[static_cast<size_t>(h) * p.M + m] = -p.lse[static_cast<size_t>(m) * p.heads + h] * kLog2e;
+  p.stat[static_cast<size_t>(p.heads + h) * p.M + m] = -s[threadIdx.x >> 5][threadIdx.x & 31];
+}
+
+// Part c of a thread's 32 packed values over its first columns.
+template <int kParts>
+__device__ __forceinline__ void attn_put_part(uint32_t taddr, int c, const uint32_t (&w)[16]) {
+  if constexpr (kParts == 1) {
+    tmem_st16(taddr, w);
+  } else {
+    uint32_t u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = w[8 * c + i];
+    tmem_st8(taddr + 8 * c, u);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -75,6 +88,10 @@ struct AttnDkvCfg {
   static constexpr int kTileBytes = kAttnTile * D * 2;
   static constexpr int kStages = D == 128 ? 2 : 4;         // of Q, and of dO
   static constexpr int kKv = D == 128 ? 1 : 2;             // of K and V
+  // P and dS are handed over in two parts where the products take longer than
+  // the elementwise work, so that they begin earlier; each hand-over costs the
+  // warps some 100 cycles.
+  static constexpr int kParts = D == 128 ? 2 : 1;
   static constexpr int kBars = 6 * kStages + 2 * kStages + 2 * kKv + 6 + 2 + 1;
   static constexpr int kSmemBytes = (2 * kKv + 2 * kStages) * kTileBytes + kStages * kAttnTile * 8 + kBars * 8 + 16 + 1024;
   static_assert(kSmemBytes <= kSmemLimitBytes, "shared memory");
@@ -87,7 +104,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
   constexpr int T = kAttnTile, S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr int NB = C::kKv;
+  constexpr int NB = C::kKv, kParts = C::kParts;
   uint8_t* sk = smem;                  // [NB]
   uint8_t* sv = sk + NB * C::kTileBytes;
   uint8_t* ring_q = sv + NB * C::kTileBytes;
@@ -213,16 +230,16 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
                      bool fresh, uint64_t* bar) {
       const uint64_t b = sdesc_sw128(smem_u32(ring), T * 128, 1024) + stage * (C::kTileBytes >> 4);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < kParts; ++c) {
         if (!mbar_wait_warp(&ready[c], parity, ctl)) return false;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < T / 32; ++k) {
-            const int kk = attn_part_step<32>(c, k);
+          for (int k = 0; k < T / 16 / kParts; ++k) {
+            const int kk = kParts == 2 ? attn_part_step<32>(c, k) : k;
             mma_bf16_ta(d, a + attn_step_column<32>(kk), b + kk * (2048 >> 4), kIdO, !fresh || c + k > 0);
           }
-          if (c == 1) mma_commit(bar);
+          if (c == kParts - 1) mma_commit(bar);
         }
       }
       return true;
@@ -287,7 +304,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int m = row + e * 32 + lane;
-          l[e] = m < t.end ? a[m] : INFINITY;
+          l[e] = m < t.end ? a[m] : -INFINITY;
           d[e] = m < t.end ? b[m] : 0.0f;
         }
         ok = mbar_wait_warp(&st_empty[r.stage], r.phase ^ 1u, ctl);
@@ -332,6 +349,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     const int quarter = (warp - 4) >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t rS = tS + lanes + 32 * quarter, rP = tP + lanes + 32 * quarter;
+    AttnScore<kCap, kBias> score(p);
+    const float2 mul = both(score.mul);
     RingPos r;
     uint32_t turn = 0, step = 0;
     while (ok && items.advance()) {
@@ -347,8 +366,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       const int key = t.row0 + (warp & 3) * 32 + lane;
       const bool all_keys = min(t.row0 + T, t.end) <= t.prefix_end;
       int h = hk * group, tile0 = first;
+      score.head(p, h);
       for (int i = 0; i < n && ok; ++i, ++step) {
-        const AttnScore<kCap, kBias> score(p, h);
         const int i0 = tile0 + 32 * quarter;                           // the first of this thread's 32 queries
         ok = mbar_wait_warp(&st_full[r.stage], r.phase, ctl) && mbar_wait_warp(s_full, step & 1u, ctl);
         if (!ok) break;
@@ -358,35 +377,37 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         float2 g[16];                     // p, then p d(cap tanh)
         tmem_ld32(rS, v[0]);
         tmem_wait_ld();
-        score.template apply<1, true, true>(v, i0 - key, g);
-        const float2 mul = both(score.mul);
+        score.template values<1, true>(v, g);
+        const float d0 = static_cast<float>(i0 - key);
         const bool part = !all_keys && tile0 < t.row0 + T;
         const int lim = key < t.prefix_end ? 0 : key - i0;             // queries from this one on see the key
+        uint32_t w[16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w[8];
+        for (int e = 0; e < 32; e += 4) {
+          const float4 l = *reinterpret_cast<const float4*>(st + e);   // -lse
+          const float2 nl[2] = {make_float2(l.x, l.y), make_float2(l.z, l.w)};
 #pragma unroll
-          for (int e = 16 * c; e < 16 * c + 16; e += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(st + e);
-            const float2 nl[2] = {make_float2(-l.x, -l.y), make_float2(-l.z, -l.w)};
+          for (int u = 0; u < 2; ++u)
+            AttnScore<kCap, kBias>::put(
+                v[0], e + 2 * u,
+                attn_exp2<kAttnBwdPoly>(fma2(pair_of(&v[0][e + 2 * u]), mul, score.shifted(nl[u], d0, e + 2 * u, 1.0f)),
+                                        e / 2 + u));
+          if (e % (32 / kParts) == 32 / kParts - 4) {
+            const int e0 = e + 4 - 32 / kParts;
+            if (part) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-              AttnScore<kCap, kBias>::put(v[0], e + 2 * u,
-                                          attn_exp2<kAttnBwdPoly>(fma2(pair_of(&v[0][e + 2 * u]), mul, nl[u]), e / 2 + u));
+              for (int k = e0; k < e + 4; ++k)
+                if (k < lim) v[0][k] = 0u;
+            }
+#pragma unroll
+            for (int k = e0; k < e + 4; k += 2) {
+              const float2 y = pair_of(&v[0][k]);
+              w[k / 2] = pack_bf16x2(y.x, y.y);
+              g[k / 2] = kCap ? mul2(y, g[k / 2]) : y;
+            }
+            attn_put_part<kParts>(rS, e0 / (32 / kParts), w);
+            attn_publish(&p_full[e0 / (32 / kParts)], lane);
           }
-          if (part) {
-#pragma unroll
-            for (int e = 16 * c; e < 16 * c + 16; ++e)
-              if (e < lim) v[0][e] = 0u;
-          }
-#pragma unroll
-          for (int e = 16 * c; e < 16 * c + 16; e += 2) {
-            const float2 y = pair_of(&v[0][e]);
-            w[e / 2 - 8 * c] = pack_bf16x2(y.x, y.y);
-            g[e / 2] = kCap ? mul2(y, g[e / 2]) : y;
-          }
-          tmem_st8(rS + 8 * c, w);
-          attn_publish(&p_full[c], lane);
         }
         ok = mbar_wait_warp(dp_full, step & 1u, ctl);
         if (!ok) break;
@@ -394,23 +415,22 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         tmem_ld32(rP, v[0]);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t w[8];
-#pragma unroll
-          for (int e = 16 * c; e < 16 * c + 16; e += 4) {
-            const float4 d = *reinterpret_cast<const float4*>(st + T + e);
-            const float2 a = mul2(g[e / 2], add2(pair_of(&v[0][e]), make_float2(-d.x, -d.y)));
-            const float2 b = mul2(g[e / 2 + 1], add2(pair_of(&v[0][e + 2]), make_float2(-d.z, -d.w)));
-            w[e / 2 - 8 * c] = pack_bf16x2(a.x, a.y);
-            w[e / 2 - 8 * c + 1] = pack_bf16x2(b.x, b.y);
+        for (int e = 0; e < 32; e += 4) {
+          const float4 d = *reinterpret_cast<const float4*>(st + T + e);   // -delta
+          const float2 a = mul2(g[e / 2], add2(pair_of(&v[0][e]), make_float2(d.x, d.y)));
+          const float2 b = mul2(g[e / 2 + 1], add2(pair_of(&v[0][e + 2]), make_float2(d.z, d.w)));
+          w[e / 2] = pack_bf16x2(a.x, a.y);
+          w[e / 2 + 1] = pack_bf16x2(b.x, b.y);
+          if (e % (32 / kParts) == 32 / kParts - 4) {
+            const int c = e / (32 / kParts);
+            attn_put_part<kParts>(rP, c, w);
+            attn_publish(&ds_full[c], lane);
           }
-          tmem_st8(rP + 8 * c, w);
-          attn_publish(&ds_full[c], lane);
         }
         if (lane == 0) mbar_arrive(&st_empty[r.stage]);
         r.next(S);
         tile0 += T;
-        if (tile0 >= t.end) { tile0 = first; ++h; }
+        if (tile0 >= t.end && i + 1 < n) { tile0 = first; score.head(p, ++h); }
       }
       ok = ok && mbar_wait_warp(acc_full, turn & 1u, ctl);
       if (!ok) break;
@@ -662,6 +682,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     const int quarter = (warp - 4) >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t rP = tP + lanes + 32 * quarter;
+    AttnScore<kCap, kBias> score(p);
+    const float2 mul = both(score.mul);
     uint32_t turn = 0, step = 0;
     while (ok && items.advance()) {
       const AttnTileRef t = items.t;
@@ -675,10 +697,10 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       const bool mine = row < t.end;
       const int see = min(max(row + 1, t.prefix_end), t.end);              // keys [begin, see)
       const int all = min(max(t.row0 + 1, t.prefix_end), t.end);           // ... that every row sees
-      const float lse2 = mine ? p.stat[static_cast<size_t>(h) * p.M + row] : INFINITY;
-      const float delta = mine ? p.stat[static_cast<size_t>(p.heads + h) * p.M + row] : 0.0f;
-      const AttnScore<kCap, kBias> score(p, h);
-      const float2 mul = both(score.mul), shift = both(-lse2);
+      const float nlse = mine ? p.stat[static_cast<size_t>(h) * p.M + row] : -INFINITY;
+      const float ndelta = mine ? p.stat[static_cast<size_t>(p.heads + h) * p.M + row] : 0.0f;
+      score.head(p, h);
+      const float2 shift = both(nlse);
       for (int j = 0; j < n && ok; ++j, ++step) {
         const int j0 = t.begin + j * T + 32 * quarter;                     // the first of this thread's 32 keys
         const uint32_t rS = tS + (step & 1u) * T + lanes + 32 * quarter;
@@ -689,10 +711,11 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         float2 g[16];                     // p d(cap tanh)
         tmem_ld32(rS, v[0]);
         tmem_wait_ld();
-        score.template apply<1, true, true>(v, j0 - row, g);
+        score.template values<1, true>(v, g);
+        const float d0 = static_cast<float>(j0 - row);
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float2 y = attn_exp2<kAttnBwdPoly>(fma2(pair_of(&v[0][e]), mul, shift), e / 2);
+          const float2 y = attn_exp2<kAttnBwdPoly>(fma2(pair_of(&v[0][e]), mul, score.shifted(shift, d0, e, 1.0f)), e / 2);
           g[e / 2] = kCap ? mul2(y, g[e / 2]) : y;
         }
         if (j0 + 32 > all) {
@@ -711,7 +734,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float2 y = mul2(g[e / 2], add2(pair_of(&v[0][e]), both(-delta)));
+          const float2 y = mul2(g[e / 2], add2(pair_of(&v[0][e]), both(ndelta)));
           w[e / 2] = pack_bf16x2(y.x, y.y);
         }
         tmem_st16(rS, w);

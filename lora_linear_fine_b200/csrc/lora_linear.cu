@@ -2314,7 +2314,7 @@ lora_status_t launch_attn_fwd(const AttnParams& p, int sms, cudaStream_t st) {
       !attn_tm(&maps.v, p.V, p, p.kv_heads, D))
     return LORA_ERR_CUDA;
   constexpr auto k = attn_fwd_kernel<D, kCap, kBias>;
-  LORA_TRY(kernel_ready<k>(AttnFwdCfg<D>::kSmemBytes, kAttnFwdThreads, 128 * (kAttnFwdRegsLow + 2 * kAttnFwdRegsHigh)));
+  LORA_TRY(kernel_ready<k>(AttnFwdCfg<D>::kSmemBytes));
   const int64_t ctas = static_cast<int64_t>(p.plan.max_fwd) * p.heads;
   if (ctas > (int64_t(1) << 31) - 1) return LORA_ERR_UNSUPPORTED;
   launch_k(k, dim3(static_cast<unsigned>(std::min<int64_t>(ctas, sms))), dim3(kAttnFwdThreads), AttnFwdCfg<D>::kSmemBytes, st, false, p, maps);
