@@ -272,6 +272,9 @@ __device__ __forceinline__ float2 attn_exp2(float2 x, int i) {
 //   denominator), within a few 2^-24.
 template <bool kCap, bool kBias>
 struct AttnScore {
+  // Of four pairs of exponentials, those by the polynomial.  With a cap or a
+  // bias the FMA pipe is the busy one already.
+  static constexpr int kPoly = kCap || kBias ? 0 : 1;
   float mul;
   float slope2 = 0.0f;
   float pre = 0.0f, limit = 0.0f, a0 = 0.0f, a1 = 0.0f, a2 = 0.0f, a3 = 0.0f;
@@ -412,4 +415,33 @@ __device__ __forceinline__ uint4 attn_pack8(const uint32_t* v, float by) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// Each lane holds n 16-byte chunks of its own row (lane i: row i of the warp's
+// 32): they change places within groups of n lanes, so that a store writes
+// whole 16 n byte pieces of 32 / n rows.  32 rows at a time, one chunk each,
+// cost the store path a cycle or two a row: 3700 cycles for a tile of dk and
+// dv.  Rows from `rows` on are left out.
+template <int n>
+__device__ __forceinline__ void attn_store_rows(uint4 (&w)[n], uint8_t* base, size_t stride, int rows, int lane) {
+#pragma unroll
+  for (int s = n / 2; s > 0; s >>= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      if (i & s) continue;
+      uint4 v = up ? w[i] : w[i | s];
+      v.x = __shfl_xor_sync(0xffffffffu, v.x, s);
+      v.y = __shfl_xor_sync(0xffffffffu, v.y, s);
+      v.z = __shfl_xor_sync(0xffffffffu, v.z, s);
+      v.w = __shfl_xor_sync(0xffffffffu, v.w, s);
+      if (up) w[i] = v;
+      else w[i | s] = v;
+    }
+  }
+  const int first = lane / n * n;
+  uint8_t* out = base + first * stride + (lane % n) * 16;
+#pragma unroll
+  for (int i = 0; i < n; ++i)
+    if (first + i < rows) *reinterpret_cast<uint4*>(out + i * stride) = w[i];
+}
+
 }  // namespace lora

@@ -16,7 +16,6 @@
 namespace lora {
 
 constexpr int kAttnBwdThreads = 640;     // warps: TMA, MMA, statistics, trimming, 16 of elementwise work
-constexpr int kAttnBwdPoly = 1;          // of four pairs of exponentials, those by the polynomial
 
 struct AttnBwdMaps {
   CUtensorMap q, k, v, d_o;   // [M x heads * D] bf16, box 64 x 128, 128-byte swizzle
@@ -210,84 +209,86 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
-    constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
-    constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
-    // a resident tile (keys) times a ring tile's rows
-    auto across = [&](const uint8_t* res, uint32_t buf, const uint8_t* ring, uint32_t stage, uint32_t d, uint64_t* bar) {
-      const uint64_t a = sdesc_sw128(smem_u32(res), 16, 1024) + buf * (C::kTileBytes >> 4);
-      const uint64_t b = sdesc_sw128(smem_u32(ring), 16, 1024) + stage * (C::kTileBytes >> 4);
-      if (elect_one()) {
+    if (elect_one()) {
+      constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
+      constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
+      // a resident tile (keys) times a ring tile's rows
+      auto across = [&](const uint8_t* res, uint32_t buf, const uint8_t* ring, uint32_t stage, uint32_t d, uint64_t* bar) {
+        const uint64_t a = sdesc_sw128(smem_u32(res), 16, 1024) + buf * (C::kTileBytes >> 4);
+        const uint64_t b = sdesc_sw128(smem_u32(ring), 16, 1024) + stage * (C::kTileBytes >> 4);
+        {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
-          mma_bf16(d, a + off, b + off, kIdS, kk > 0);
-        }
-        mma_commit(bar);
-      }
-    };
-    // tensor memory (keys x queries) times a ring tile, which is free afterwards
-    auto along = [&](uint32_t a, uint64_t* ready, uint32_t parity, const uint8_t* ring, uint32_t stage, uint32_t d,
-                     bool fresh, uint64_t* bar) {
-      const uint64_t b = sdesc_sw128(smem_u32(ring), T * 128, 1024) + stage * (C::kTileBytes >> 4);
-#pragma unroll
-      for (int c = 0; c < kParts; ++c) {
-        if (!mbar_wait_warp(&ready[c], parity, ctl)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < T / 16 / kParts; ++k) {
-            const int kk = kParts == 2 ? attn_part_step<32>(c, k) : k;
-            mma_bf16_ta(d, a + attn_step_column<32>(kk), b + kk * (2048 >> 4), kIdO, !fresh || c + k > 0);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
+            mma_bf16(d, a + off, b + off, kIdS, kk > 0);
           }
-          if (c == kParts - 1) mma_commit(bar);
+          mma_commit(bar);
         }
-      }
-      return true;
-    };
-    RingPos r;
-    uint32_t turn = 0, step = 0;
-    while (ok && items.advance()) {
-      if (items.behind()) continue;
-      const int n = (items.t.end - first_of() + T - 1) / T * group;
-      const uint32_t buf = turn % NB;
-      ok = mbar_wait_warp(&kv_full[buf], (turn / NB) & 1u, ctl) && mbar_wait_warp(&q_full[r.stage], r.phase, ctl);
-      if (!ok) break;
-      tc_fence_after();
-      across(sk, buf, ring_q, r.stage, tS, s_full);
-      ok = mbar_wait_warp(&o_full[r.stage], r.phase, ctl);
-      if (!ok) break;
-      tc_fence_after();
-      across(sv, buf, ring_o, r.stage, tP, dp_full);
-      if (n == 1 && elect_one()) mma_commit(&kv_empty[buf]);
-      // the accumulators of the item before have been read
-      ok = mbar_wait_warp(acc_empty, (turn & 1u) ^ 1u, ctl);
-      for (int i = 0; i < n && ok; ++i, ++step) {
-        RingPos nx = r;
-        nx.next(S);
-        ok = along(tS, p_full, step & 1u, ring_o, r.stage, tV, i == 0, &o_empty[r.stage]);
-        if (!ok) break;
-        if (i + 1 < n) {
-          ok = mbar_wait_warp(&q_full[nx.stage], nx.phase, ctl);
-          if (!ok) break;
+      };
+      // tensor memory (keys x queries) times a ring tile, which is free afterwards
+      auto along = [&](uint32_t a, uint64_t* ready, uint32_t parity, const uint8_t* ring, uint32_t stage, uint32_t d,
+                       bool fresh, uint64_t* bar) {
+        const uint64_t b = sdesc_sw128(smem_u32(ring), T * 128, 1024) + stage * (C::kTileBytes >> 4);
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) {
+          if (!mbar_wait(&ready[c], parity, ctl)) return false;
           tc_fence_after();
-          across(sk, buf, ring_q, nx.stage, tS, s_full);
+          {
+#pragma unroll
+            for (int k = 0; k < T / 16 / kParts; ++k) {
+              const int kk = kParts == 2 ? attn_part_step<32>(c, k) : k;
+              mma_bf16_ta(d, a + attn_step_column<32>(kk), b + kk * (2048 >> 4), kIdO, !fresh || c + k > 0);
+            }
+            if (c == kParts - 1) mma_commit(bar);
+          }
         }
-        ok = along(tP, ds_full, step & 1u, ring_q, r.stage, tK, i == 0, &q_empty[r.stage]);
+        return true;
+      };
+      RingPos r;
+      uint32_t turn = 0, step = 0;
+      while (ok && items.advance()) {
+        if (items.behind()) continue;
+        const int n = (items.t.end - first_of() + T - 1) / T * group;
+        const uint32_t buf = turn % NB;
+        ok = mbar_wait(&kv_full[buf], (turn / NB) & 1u, ctl) && mbar_wait(&q_full[r.stage], r.phase, ctl);
         if (!ok) break;
-        if (i + 1 < n) {
-          ok = mbar_wait_warp(&o_full[nx.stage], nx.phase, ctl);
+        tc_fence_after();
+        across(sk, buf, ring_q, r.stage, tS, s_full);
+        ok = mbar_wait(&o_full[r.stage], r.phase, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        across(sv, buf, ring_o, r.stage, tP, dp_full);
+        if (n == 1) mma_commit(&kv_empty[buf]);
+        // the accumulators of the item before have been read
+        ok = mbar_wait(acc_empty, (turn & 1u) ^ 1u, ctl);
+        for (int i = 0; i < n && ok; ++i, ++step) {
+          RingPos nx = r;
+          nx.next(S);
+          ok = along(tS, p_full, step & 1u, ring_o, r.stage, tV, i == 0, &o_empty[r.stage]);
           if (!ok) break;
-          tc_fence_after();
-          across(sv, buf, ring_o, nx.stage, tP, dp_full);
-          if (i + 2 == n && elect_one()) mma_commit(&kv_empty[buf]);
+          if (i + 1 < n) {
+            ok = mbar_wait(&q_full[nx.stage], nx.phase, ctl);
+            if (!ok) break;
+            tc_fence_after();
+            across(sk, buf, ring_q, nx.stage, tS, s_full);
+          }
+          ok = along(tP, ds_full, step & 1u, ring_q, r.stage, tK, i == 0, &q_empty[r.stage]);
+          if (!ok) break;
+          if (i + 1 < n) {
+            ok = mbar_wait(&o_full[nx.stage], nx.phase, ctl);
+            if (!ok) break;
+            tc_fence_after();
+            across(sv, buf, ring_o, nx.stage, tP, dp_full);
+            if (i + 2 == n) mma_commit(&kv_empty[buf]);
+          }
+          r = nx;
         }
-        r = nx;
+        if (ok) mma_commit(acc_full);
+        ++turn;
       }
-      if (ok && elect_one()) mma_commit(acc_full);
-      ++turn;
+      mma_commit(mma_done);
+      mbar_wait(mma_done, 0, quiet);
     }
-    if (elect_one()) mma_commit(mma_done);
-    mbar_wait_warp(mma_done, 0, quiet);
   } else if (warp == 2) {
     // ---------------------------------------------------------------- row statistics
     // Rows past the document: lse = infinity makes their p zero.
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
           for (int u = 0; u < 2; ++u)
             AttnScore<kCap, kBias>::put(
                 v[0], e + 2 * u,
-                attn_exp2<kAttnBwdPoly>(fma2(pair_of(&v[0][e + 2 * u]), mul, score.shifted(nl[u], d0, e + 2 * u, 1.0f)),
+                attn_exp2<AttnScore<kCap, kBias>::kPoly>(fma2(pair_of(&v[0][e + 2 * u]), mul, score.shifted(nl[u], d0, e + 2 * u, 1.0f)),
                                         e / 2 + u));
           if (e % (32 / kParts) == 32 / kParts - 4) {
             const int e0 = e + 4 - 32 / kParts;
@@ -452,11 +453,10 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty);
-      if (key < t.end) {
-        uint4* out = reinterpret_cast<uint4*>((is_k ? p.dK : p.dV) + (static_cast<size_t>(key) * p.kv_heads + hk) * D + f0);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) out[k] = w[k];
-      }
+      const int key0 = key - lane;               // the warp's first
+      const size_t stride = static_cast<size_t>(p.kv_heads) * D * 2;
+      attn_store_rows<D / 16>(w, reinterpret_cast<uint8_t*>(is_k ? p.dK : p.dV) + key0 * stride +
+                                     (static_cast<size_t>(hk) * D + f0) * 2, stride, t.end - key0, lane);
     }
   }
 
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     mbar_init(qo_full, 1);
     mbar_init(qo_empty, 1);
     mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 16);
+    mbar_init(acc_empty, 4 * (D / 32));
     mbar_init(&s_full[0], 1);
     mbar_init(&s_full[1], 1);
     mbar_init(dp_full, 1);
@@ -589,72 +589,74 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA
-    constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
-    constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
-    auto across = [&](const uint8_t* res, const uint8_t* ring, uint32_t stage, uint32_t d, uint64_t* bar, uint64_t* bar2) {
-      const uint64_t a = sdesc_sw128(smem_u32(res), 16, 1024);
-      const uint64_t b = sdesc_sw128(smem_u32(ring), 16, 1024) + stage * (C::kTileBytes >> 4);
-      if (elect_one()) {
+    if (elect_one()) {
+      constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
+      constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
+      auto across = [&](const uint8_t* res, const uint8_t* ring, uint32_t stage, uint32_t d, uint64_t* bar, uint64_t* bar2) {
+        const uint64_t a = sdesc_sw128(smem_u32(res), 16, 1024);
+        const uint64_t b = sdesc_sw128(smem_u32(ring), 16, 1024) + stage * (C::kTileBytes >> 4);
+        {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
-          mma_bf16(d, a + off, b + off, kIdS, kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
+            mma_bf16(d, a + off, b + off, kIdS, kk > 0);
+          }
+          mma_commit(bar);
+          if (bar2 != nullptr) mma_commit(bar2);
         }
-        mma_commit(bar);
-        if (bar2 != nullptr) mma_commit(bar2);
-      }
-    };
-    RingPos ks, kd, v;             // K tiles of the scores, of dQ; V tiles
-    uint32_t turn = 0, issued = 0, step = 0;      // items; score tiles issued; dS tiles taken
-    auto scores = [&]() {
-      if (!mbar_wait_warp(&k_full[ks.stage], ks.phase, ctl)) return false;
-      tc_fence_after();
-      across(sq, ring_k, ks.stage, tS + (issued & 1u) * T, &s_full[issued & 1u], nullptr);
-      ++issued;
-      ks.next(SK);
-      return true;
-    };
-    auto values = [&]() {
-      if (!mbar_wait_warp(&v_full[v.stage], v.phase, ctl)) return false;
-      tc_fence_after();
-      across(so, ring_v, v.stage, tP, dp_full, &v_empty[v.stage]);
-      v.next(SV);
-      return true;
-    };
-    while (ok && items.advance()) {
-      if (items.behind()) continue;
-      const int n = attn_key_tiles(items.t, items.t.row0, T);
-      ok = mbar_wait_warp(qo_full, turn & 1u, ctl);
-      ok = ok && scores() && values();
-      if (n > 1) ok = ok && scores();
-      if (ok && n == 1 && elect_one()) mma_commit(qo_empty);
-      // the accumulator of the item before has been read
-      ok = ok && mbar_wait_warp(acc_empty, (turn & 1u) ^ 1u, ctl);
-      for (int j = 0; j < n && ok; ++j, ++step) {
-        ok = mbar_wait_warp(ds_full, step & 1u, ctl);
-        if (!ok) break;
+      };
+      RingPos ks, kd, v;             // K tiles of the scores, of dQ; V tiles
+      uint32_t turn = 0, issued = 0, step = 0;      // items; score tiles issued; dS tiles taken
+      auto scores = [&]() {
+        if (!mbar_wait(&k_full[ks.stage], ks.phase, ctl)) return false;
         tc_fence_after();
-        if (j + 1 < n) {
-          ok = values();
+        across(sq, ring_k, ks.stage, tS + (issued & 1u) * T, &s_full[issued & 1u], nullptr);
+        ++issued;
+        ks.next(SK);
+        return true;
+      };
+      auto values = [&]() {
+        if (!mbar_wait(&v_full[v.stage], v.phase, ctl)) return false;
+        tc_fence_after();
+        across(so, ring_v, v.stage, tP, dp_full, &v_empty[v.stage]);
+        v.next(SV);
+        return true;
+      };
+      while (ok && items.advance()) {
+        if (items.behind()) continue;
+        const int n = attn_key_tiles(items.t, items.t.row0, T);
+        ok = mbar_wait(qo_full, turn & 1u, ctl);
+        ok = ok && scores() && values();
+        if (n > 1) ok = ok && scores();
+        if (ok && n == 1) mma_commit(qo_empty);
+        // the accumulator of the item before has been read
+        ok = ok && mbar_wait(acc_empty, (turn & 1u) ^ 1u, ctl);
+        for (int j = 0; j < n && ok; ++j, ++step) {
+          ok = mbar_wait(ds_full, step & 1u, ctl);
           if (!ok) break;
-          if (j + 2 == n && elect_one()) mma_commit(qo_empty);       // the last use of Q and dO
-        }
-        const uint64_t b = sdesc_sw128(smem_u32(ring_k), T * 128, 1024) + kd.stage * (C::kTileBytes >> 4);
-        const uint32_t a = tS + (step & 1u) * T;
-        if (elect_one()) {
+          tc_fence_after();
+          if (j + 1 < n) {
+            ok = values();
+            if (!ok) break;
+            if (j + 2 == n) mma_commit(qo_empty);       // the last use of Q and dO
+          }
+          const uint64_t b = sdesc_sw128(smem_u32(ring_k), T * 128, 1024) + kd.stage * (C::kTileBytes >> 4);
+          const uint32_t a = tS + (step & 1u) * T;
+          {
 #pragma unroll
-          for (int kk = 0; kk < T / 16; ++kk)
-            mma_bf16_ta(tQ, a + attn_step_column<32>(kk), b + kk * (2048 >> 4), kIdO, j > 0 || kk > 0);
-          mma_commit(&k_empty[kd.stage]);
+            for (int kk = 0; kk < T / 16; ++kk)
+              mma_bf16_ta(tQ, a + attn_step_column<32>(kk), b + kk * (2048 >> 4), kIdO, j > 0 || kk > 0);
+            mma_commit(&k_empty[kd.stage]);
+          }
+          kd.next(SK);
+          if (j + 2 < n) ok = scores();
         }
-        kd.next(SK);
-        if (j + 2 < n) ok = scores();
+        if (ok) mma_commit(acc_full);
+        ++turn;
       }
-      if (ok && elect_one()) mma_commit(acc_full);
-      ++turn;
+      mma_commit(mma_done);
+      mbar_wait(mma_done, 0, quiet);
     }
-    if (elect_one()) mma_commit(mma_done);
-    mbar_wait_warp(mma_done, 0, quiet);
   } else if (warp == 2) {
     // ---------------------------------------------------------------- trimming
     uint32_t slot = 0, k_landed = 0, v_landed = 0;
@@ -715,7 +717,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         const float d0 = static_cast<float>(j0 - row);
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float2 y = attn_exp2<kAttnBwdPoly>(fma2(pair_of(&v[0][e]), mul, score.shifted(shift, d0, e, 1.0f)), e / 2);
+          const float2 y = attn_exp2<AttnScore<kCap, kBias>::kPoly>(fma2(pair_of(&v[0][e]), mul, score.shifted(shift, d0, e, 1.0f)), e / 2);
           g[e / 2] = kCap ? mul2(y, g[e / 2]) : y;
         }
         if (j0 + 32 > all) {
@@ -744,22 +746,22 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       if (!ok) break;
       ++turn;
       tc_fence_after();
-      uint4 w[D / 32];
-#pragma unroll
-      for (int c = 0; c < D / 4; c += 16) {
-        uint32_t o[16];
-        tmem_ld16(tQ + lanes + quarter * (D / 4) + c, o);
+      // 64-byte pieces of a row: by all warps, or by the first half of them
+      constexpr int kPieces = D / 32;
+      if (quarter < kPieces) {
+        uint32_t o[32];
+        tmem_ld32(tQ + lanes + 32 * quarter, o);
         tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty);
+        uint4 w[4];
 #pragma unroll
-        for (int e = 0; e < 16; e += 8) w[(c + e) / 8] = attn_pack8(&o[e], p.scale);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty);
-      if (mine) {
-        uint4* out = reinterpret_cast<uint4*>(p.dQ + (static_cast<size_t>(row) * p.heads + h) * D + quarter * (D / 4));
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) out[k] = w[k];
+        for (int e = 0; e < 32; e += 8) w[e / 8] = attn_pack8(&o[e], p.scale);
+        const int row0 = row - lane;
+        const size_t stride = static_cast<size_t>(p.heads) * D * 2;
+        attn_store_rows<4>(w, reinterpret_cast<uint8_t*>(p.dQ) + row0 * stride +
+                                  (static_cast<size_t>(h) * D + 32 * quarter) * 2, stride, t.end - row0, lane);
       }
     }
   }

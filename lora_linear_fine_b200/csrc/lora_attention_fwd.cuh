@@ -42,7 +42,6 @@ struct AttnFwdCfg {
   static constexpr int kSmemBytes = (2 + kStages) * kTileBytes + kBars * 8 + 16 + 1024;
   static_assert(kSmemBytes <= kSmemLimitBytes, "shared memory");
 };
-constexpr int kAttnFwdPoly = 1;          // of four pairs of exponentials, those by the polynomial
 constexpr int kAttnFwdThreads = 384;     // warps: TMA, MMA, trimming, one idle, softmax of tile a (4), of tile b (4)
 
 struct AttnFwdMaps {
@@ -53,7 +52,7 @@ template <int D, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kAttnFwdThreads, 1)
     attn_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnFwdMaps maps) {
   using C = AttnFwdCfg<D>;
-  constexpr int T = kAttnTile, S = C::kStages;
+  constexpr int T = kAttnTile, S = C::kStages, kPoly = AttnScore<kCap, kBias>::kPoly;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem + 2 * C::kTileBytes;
@@ -150,97 +149,99 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
       }
     } else if (warp == 1) {
       // -------------------------------------------------------------- MMA
-      constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
-      constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
-      const uint64_t q_desc = sdesc_sw128(smem_u32(smem), 16, 1024);
-      const uint64_t k_desc = sdesc_sw128(smem_u32(ring), 16, 1024);
-      const uint64_t v_desc = sdesc_sw128(smem_u32(ring), T * 128, 1024);
-      auto scores = [&](int x, uint32_t stage) {
-        const uint64_t a = q_desc + x * (C::kTileBytes >> 4), b = k_desc + stage * (C::kTileBytes >> 4);
-        if (elect_one()) {
+      if (elect_one()) {
+        constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
+        constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
+        const uint64_t q_desc = sdesc_sw128(smem_u32(smem), 16, 1024);
+        const uint64_t k_desc = sdesc_sw128(smem_u32(ring), 16, 1024);
+        const uint64_t v_desc = sdesc_sw128(smem_u32(ring), T * 128, 1024);
+        auto scores = [&](int x, uint32_t stage) {
+          const uint64_t a = q_desc + x * (C::kTileBytes >> 4), b = k_desc + stage * (C::kTileBytes >> 4);
+          {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
-            mma_bf16(tbase + x * T, a + off, b + off, kIdS, kk > 0);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
+              mma_bf16(tbase + x * T, a + off, b + off, kIdS, kk > 0);
+            }
+            mma_commit(&s_full[x]);
           }
-          mma_commit(&s_full[x]);
-        }
-      };
-      // half of the keys: 4 steps of 16
-      auto values = [&](int x, uint32_t stage, int half, bool first) {
-        const uint64_t b = v_desc + stage * (C::kTileBytes >> 4);
-        if (elect_one()) {
+        };
+        // half of the keys: 4 steps of 16
+        auto values = [&](int x, uint32_t stage, int half, bool first) {
+          const uint64_t b = v_desc + stage * (C::kTileBytes >> 4);
+          {
 #pragma unroll
-          for (int k = 0; k < T / 32; ++k) {
-            const int kk = half * (T / 32) + k;
-            mma_bf16_ta(tbase + 256 + x * T, tbase + x * T + 8 * kk, b + kk * (2048 >> 4), kIdO, !first || kk > 0);
+            for (int k = 0; k < T / 32; ++k) {
+              const int kk = half * (T / 32) + k;
+              mma_bf16_ta(tbase + 256 + x * T, tbase + x * T + 8 * kk, b + kk * (2048 >> 4), kIdO, !first || kk > 0);
+            }
+            if (half == 1) mma_commit(&pv_done[x]);
           }
-          if (half == 1) mma_commit(&pv_done[x]);
-        }
-      };
-      RingPos rp;
-      uint32_t q_turn = 0, o_turn[2] = {0, 0}, step[2] = {0, 0};      // of Q; of O; key tiles of a and b
-      while (ok && items.advance()) {
-        if (items.behind()) continue;
-        const int tiles_x = items.t.row0 + T < items.t.end ? 2 : 1;
-        int n_a;
-        const int n = tiles_of(&n_a);
-        // tile a begins with its own first key tile, which may be b's second
-        const int skip = n - n_a;
-        ok = mbar_wait_warp(q_full, q_turn & 1u, ctl) && mbar_wait_warp(&full[rp.stage], rp.phase, ctl);
-        if (!ok) break;
-        ++q_turn;
-        tc_fence_after();
-        RingPos v = rp;
-        v.next(S);
-        RingPos k = v;
-        k.next(S);
-        if (skip == 0) scores(0, rp.stage);
-        if (tiles_x == 2) scores(1, rp.stage);
-        if (elect_one()) mma_commit(&empty[rp.stage]);
-        if (n == 1 && elect_one()) mma_commit(q_empty);
-        ok = mbar_wait_warp(&full[v.stage], v.phase, ctl);
-        if (n > 1) ok = ok && mbar_wait_warp(&full[k.stage], k.phase, ctl);
-        tc_fence_after();
-        for (int j = 0; j < n && ok; ++j) {
-          // the next turn's tiles, waited for while there is time
-          RingPos v2 = k, k2 = k;
-          v2.next(S);
-          k2.next(S);
-          k2.next(S);
+        };
+        RingPos rp;
+        uint32_t q_turn = 0, o_turn[2] = {0, 0}, step[2] = {0, 0};      // of Q; of O; key tiles of a and b
+        while (ok && items.advance()) {
+          if (items.behind()) continue;
+          const int tiles_x = items.t.row0 + T < items.t.end ? 2 : 1;
+          int n_a;
+          const int n = tiles_of(&n_a);
+          // tile a begins with its own first key tile, which may be b's second
+          const int skip = n - n_a;
+          ok = mbar_wait(q_full, q_turn & 1u, ctl) && mbar_wait(&full[rp.stage], rp.phase, ctl);
+          if (!ok) break;
+          ++q_turn;
+          tc_fence_after();
+          RingPos v = rp;
+          v.next(S);
+          RingPos k = v;
+          k.next(S);
+          if (skip == 0) scores(0, rp.stage);
+          if (tiles_x == 2) scores(1, rp.stage);
+          mma_commit(&empty[rp.stage]);
+          if (n == 1) mma_commit(q_empty);
+          ok = mbar_wait(&full[v.stage], v.phase, ctl);
+          if (n > 1) ok = ok && mbar_wait(&full[k.stage], k.phase, ctl);
+          tc_fence_after();
+          for (int j = 0; j < n && ok; ++j) {
+            // the next turn's tiles, waited for while there is time
+            RingPos v2 = k, k2 = k;
+            v2.next(S);
+            k2.next(S);
+            k2.next(S);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int from = x == 0 ? skip : 0;
-            if (ok && j >= from && x < tiles_x) {
-              if (j == from) ok = mbar_wait_warp(&o_empty[x], (o_turn[x]++ & 1u) ^ 1u, ctl);
+            for (int x = 0; x < 2; ++x) {
+              const int from = x == 0 ? skip : 0;
+              if (ok && j >= from && x < tiles_x) {
+                if (j == from) ok = mbar_wait(&o_empty[x], (o_turn[x]++ & 1u) ^ 1u, ctl);
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                ok = ok && mbar_wait_warp(&p_full[2 * x + half], step[x] & 1u, ctl);
-                if (!ok) break;
-                tc_fence_after();
-                values(x, v.stage, half, j == from);
+                for (int half = 0; half < 2; ++half) {
+                  ok = ok && mbar_wait(&p_full[2 * x + half], step[x] & 1u, ctl);
+                  if (!ok) break;
+                  tc_fence_after();
+                  values(x, v.stage, half, j == from);
+                }
+                ++step[x];
               }
-              ++step[x];
+              if (ok && j + 1 >= from && j + 1 < n && x < tiles_x) scores(x, k.stage);
+              if (x == 0 && ok && j + 1 < n) {
+                ok = mbar_wait(&full[v2.stage], v2.phase, ctl);
+                if (j + 2 < n) ok = ok && mbar_wait(&full[k2.stage], k2.phase, ctl);
+                tc_fence_after();
+              }
             }
-            if (ok && j + 1 >= from && j + 1 < n && x < tiles_x) scores(x, k.stage);
-            if (x == 0 && ok && j + 1 < n) {
-              ok = mbar_wait_warp(&full[v2.stage], v2.phase, ctl);
-              if (j + 2 < n) ok = ok && mbar_wait_warp(&full[k2.stage], k2.phase, ctl);
-              tc_fence_after();
+            if (ok) {
+              mma_commit(&empty[v.stage]);
+              if (j + 1 < n) mma_commit(&empty[k.stage]);
+              if (j + 2 == n) mma_commit(q_empty);        // the last scores have been issued
             }
+            rp = k;
+            v = v2;
+            k = k2;
           }
-          if (ok && elect_one()) {
-            mma_commit(&empty[v.stage]);
-            if (j + 1 < n) mma_commit(&empty[k.stage]);
-            if (j + 2 == n) mma_commit(q_empty);        // the last scores have been issued
-          }
-          rp = k;
-          v = v2;
-          k = k2;
         }
+        mma_commit(mma_done);
+        mbar_wait(mma_done, 0, quiet);
       }
-      if (elect_one()) mma_commit(mma_done);
-      mbar_wait_warp(mma_done, 0, quiet);
     } else if (warp == 2) {
       // -------------------------------------------------------------- trimming
       uint32_t slot = 0, landed = 0;         // ring slots so far; a bit a stage: parity of its next landing
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float2 y = attn_exp2<kAttnFwdPoly>(
+              const float2 y = attn_exp2<kPoly>(
                   fma2(pair_of(&v[c][e]), mul, score.shifted(shift, d0 + 64 * half, 32 * c + e, 1.0f)), e / 2);
               sum[(e / 2) & 1] = add2(sum[(e / 2) & 1], y);
               w[e / 2] = pack_bf16x2(y.x, y.y);
@@ -401,22 +402,28 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const float total = l.x + l.y, inv = 1.0f / total;
-      uint4 w[D / 8];
+      const int row0 = row - lane;               // the warp's first
+      const size_t stride = static_cast<size_t>(p.heads) * D * 2;
+      uint8_t* out = reinterpret_cast<uint8_t*>(p.O) + row0 * stride + static_cast<size_t>(h) * D * 2;
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(tO + c, o);
-        tmem_wait_ld();
+      for (int f = 0; f < D; f += 64) {
+        uint4 w[8];
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) w[(c + e) / 8] = attn_pack8(&o[e], inv);
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + f + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) w[(c + e) / 8] = attn_pack8(&o[e], inv);
+        }
+        if (f + 64 == D) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&o_empty[x]);
+        }
+        attn_store_rows<8>(w, out + f * 2, stride, t.end - row0, lane);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&o_empty[x]);
       if (row < t.end) {
-        uint4* out = reinterpret_cast<uint4*>(p.O + (static_cast<size_t>(row) * p.heads + h) * D);
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) out[k] = w[k];
         // natural logarithm of sum exp z
         p.lse[static_cast<size_t>(row) * p.heads + h] = (m + log2f(total)) * 0.69314718056f;
       }
