@@ -151,6 +151,8 @@ struct AttnParams {
   __nv_bfloat16 *O, *dQ, *dK, *dV;
   float* lse;                    // [M x heads]
   float* stat;                   // backward: [2][heads][M], lse log2(e) and delta
+  float* partial;                // backward: [parts][2][M x kv_heads * D] sums of dk and dv (parts > 1)
+  int parts;
   int M, n_docs, heads, kv_heads;
   float scale, cap;              // cap 0: none
 };

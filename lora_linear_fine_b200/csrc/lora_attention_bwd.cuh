@@ -79,8 +79,13 @@ __device__ __forceinline__ void attn_put_part(uint32_t taddr, int c, const uint3
 //   S = K Q_i^T, dP = V dO_i^T      both operands in shared memory
 //   P = exp2(S - lse), dS = P (dP - delta)    512 threads, a row and 32 queries each
 //   dV += P dO_i, dK += dS Q_i      P and dS read from tensor memory
-// The products are issued as dV_i, S_i+1, dK_i, dP_i+1: while the elementwise
-// work is at dS_i the tensor core does the first two, at P_i+1 the other two.
+// The products are issued as dV_i, S_i+1, dK_i, dP_i+1 (S_i+1 first where it
+// has a buffer of its own): while the elementwise work is at dS_i the tensor
+// core does the first two, at P_i+1 the other two.
+//
+// Few key tiles and heads leave SMs idle, or wait for the longest: then the
+// steps of an item are cut into p.parts items that write fp32 sums, and
+// attn_join_kernel adds these in order.
 template <int D>
 struct AttnDkvCfg {
   static constexpr int kBoxes = D / 64;
@@ -91,7 +96,10 @@ struct AttnDkvCfg {
   // the elementwise work, so that they begin earlier; each hand-over costs the
   // warps some 100 cycles.
   static constexpr int kParts = D == 128 ? 2 : 1;
-  static constexpr int kBars = 6 * kStages + 2 * kStages + 2 * kKv + 6 + 2 + 1;
+  // Buffers of S: with two the scores of the next tile are ready before this
+  // one's work ends; with 128 features dk and dv leave room for one.
+  static constexpr int kScores = D == 128 ? 1 : 2;
+  static constexpr int kBars = 6 * kStages + 2 * kStages + 2 * kKv + 5 + kScores + 2 + 1;
   static constexpr int kSmemBytes = (2 * kKv + 2 * kStages) * kTileBytes + kStages * kAttnTile * 8 + kBars * 8 + 16 + 1024;
   static_assert(kSmemBytes <= kSmemLimitBytes, "shared memory");
 };
@@ -103,7 +111,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
   constexpr int T = kAttnTile, S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr int NB = C::kKv, kParts = C::kParts;
+  constexpr int NB = C::kKv, kParts = C::kParts, NS = C::kScores;
   uint8_t* sk = smem;                  // [NB]
   uint8_t* sv = sk + NB * C::kTileBytes;
   uint8_t* ring_q = sv + NB * C::kTileBytes;
@@ -119,8 +127,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
   uint64_t* st_empty = st_full + S;
   uint64_t* kv_full = st_empty + S;    // [NB]
   uint64_t* kv_empty = kv_full + NB;   // [NB]
-  uint64_t* s_full = kv_empty + NB;
-  uint64_t* p_full = s_full + 1;       // [2] parts of P from all warps
+  uint64_t* s_full = kv_empty + NB;    // [NS]
+  uint64_t* p_full = s_full + NS;      // [2] parts of P from all warps
   uint64_t* dp_full = p_full + 2;
   uint64_t* ds_full = dp_full + 1;     // [2]
   uint64_t* acc_full = ds_full + 2;    // dk and dv of the item are complete
@@ -139,7 +147,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       mbar_init(&st_empty[i], 16);
     }
     for (int i = 0; i < NB; ++i) { mbar_init(&kv_full[i], 1); mbar_init(&kv_empty[i], 1); }
-    mbar_init(s_full, 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&s_full[i], 1);
     mbar_init(dp_full, 1);
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, 16);
@@ -153,14 +161,30 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  const uint32_t tK = tbase, tV = tbase + D, tS = tbase + 256, tP = tbase + 384;
+  const uint32_t tK = tbase, tV = tbase + D, tS = tbase + 2 * D, tP = tbase + 2 * D + NS * T;
   grid_dep_wait();
 
-  AttnItems items(p.plan.kv, attn_plan_ok(p) ? p.plan.head[kPlanKv] : 0u, p.kv_heads);
+  AttnItems items(p.plan.kv, attn_plan_ok(p) ? p.plan.head[kPlanKv] : 0u, p.kv_heads * p.parts);
   const int group = p.heads / p.kv_heads;
   bool ok = true;
-  // query tiles that see the item's keys: from the first one with a prefix, else from the keys' own
-  auto first_of = [&] { return items.t.row0 < items.t.prefix_end ? items.t.begin : items.t.row0; };
+  // The item's steps: query heads of the group times the query tiles that see
+  // the keys (from the first one with a prefix, else from the keys' own), or
+  // its share of them.
+  struct Steps { int hk, part, first, n_tiles, n, h, row; };
+  auto steps = [&] {
+    Steps s;
+    s.hk = items.h / p.parts;
+    s.part = items.h - s.hk * p.parts;
+    s.first = items.t.row0 < items.t.prefix_end ? items.t.begin : items.t.row0;
+    s.n_tiles = (items.t.end - s.first + T - 1) / T;
+    const long long all = static_cast<long long>(s.n_tiles) * group;
+    const int from = static_cast<int>(all * s.part / p.parts);
+    s.n = static_cast<int>(all * (s.part + 1) / p.parts) - from;
+    const int g = from / s.n_tiles;
+    s.h = s.hk * group + g;
+    s.row = s.first + (from - g * s.n_tiles) * T;
+    return s;
+  };
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA
@@ -170,9 +194,10 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       while (ok && items.advance()) {
         if (items.behind()) continue;
         const AttnTileRef t = items.t;
-        const int hk = items.h, first = first_of(), n_tiles = (t.end - first + T - 1) / T;
-        int h = hk * group, row = first;
-        for (int i = 0; i < n_tiles * group && ok; ++i) {
+        const Steps st = steps();
+        const int hk = st.hk, first = st.first;
+        int h = st.h, row = st.row;
+        for (int i = 0; i < st.n && ok; ++i) {
           const bool trim = row + T > t.end;
           for (int k = 0; k < 2 && ok; ++k) {
             ok = mbar_wait(k == 0 ? &q_empty[rq.stage] : &o_empty[rq.stage], rq.phase ^ 1u, ctl);
@@ -248,31 +273,34 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       uint32_t turn = 0, step = 0;
       while (ok && items.advance()) {
         if (items.behind()) continue;
-        const int n = (items.t.end - first_of() + T - 1) / T * group;
+        const int n = steps().n;
+        if (n == 0) continue;
         const uint32_t buf = turn % NB;
         ok = mbar_wait(&kv_full[buf], (turn / NB) & 1u, ctl) && mbar_wait(&q_full[r.stage], r.phase, ctl);
         if (!ok) break;
         tc_fence_after();
-        across(sk, buf, ring_q, r.stage, tS, s_full);
+        across(sk, buf, ring_q, r.stage, tS + step % NS * T, &s_full[step % NS]);
         ok = mbar_wait(&o_full[r.stage], r.phase, ctl);
         if (!ok) break;
         tc_fence_after();
         across(sv, buf, ring_o, r.stage, tP, dp_full);
         if (n == 1) mma_commit(&kv_empty[buf]);
-        // the accumulators of the item before have been read
-        ok = mbar_wait(acc_empty, (turn & 1u) ^ 1u, ctl);
         for (int i = 0; i < n && ok; ++i, ++step) {
           RingPos nx = r;
           nx.next(S);
-          ok = along(tS, p_full, step & 1u, ring_o, r.stage, tV, i == 0, &o_empty[r.stage]);
-          if (!ok) break;
-          if (i + 1 < n) {
-            ok = mbar_wait(&q_full[nx.stage], nx.phase, ctl);
-            if (!ok) break;
+          const uint32_t tA = tS + step % NS * T, next = (step + 1) % NS;
+          auto next_scores = [&] {
+            if (!mbar_wait(&q_full[nx.stage], nx.phase, ctl)) return false;
             tc_fence_after();
-            across(sk, buf, ring_q, nx.stage, tS, s_full);
-          }
-          ok = along(tP, ds_full, step & 1u, ring_q, r.stage, tK, i == 0, &q_empty[r.stage]);
+            across(sk, buf, ring_q, nx.stage, tS + next * T, &s_full[next]);
+            return true;
+          };
+          if (NS == 2 && i + 1 < n) ok = next_scores();
+          // the accumulators of the item before have been read
+          if (i == 0) ok = ok && mbar_wait(acc_empty, (turn & 1u) ^ 1u, ctl);
+          ok = ok && along(tA, p_full, step & 1u, ring_o, r.stage, tV, i == 0, &o_empty[r.stage]);
+          if (NS == 1 && i + 1 < n) ok = ok && next_scores();
+          ok = ok && along(tP, ds_full, step & 1u, ring_q, r.stage, tK, i == 0, &q_empty[r.stage]);
           if (!ok) break;
           if (i + 1 < n) {
             ok = mbar_wait(&o_full[nx.stage], nx.phase, ctl);
@@ -296,9 +324,10 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     while (ok && items.advance()) {
       if (items.behind()) continue;
       const AttnTileRef t = items.t;
-      const int first = first_of(), n = (t.end - first + T - 1) / T * group;
-      int h = items.h * group, row = first;
-      for (int i = 0; i < n && ok; ++i) {
+      const Steps st = steps();
+      const int first = st.first;
+      int h = st.h, row = st.row;
+      for (int i = 0; i < st.n && ok; ++i) {
         const float* a = p.stat + static_cast<size_t>(h) * p.M;
         const float* b = a + static_cast<size_t>(p.heads) * p.M;
         float l[4], d[4];
@@ -331,10 +360,12 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     while (ok && items.advance()) {
       if (items.behind()) continue;
       const AttnTileRef t = items.t;
-      const int first = first_of(), n_tiles = (t.end - first + T - 1) / T;
-      const int keep = (t.end - first) % T;
-      for (int g = 0; g < group && ok && keep != 0; ++g) {
-        const uint32_t stage = (slot + n_tiles * (g + 1) - 1) % S;
+      const Steps st = steps();
+      const int keep = (t.end - st.first) % T;
+      // steps of the document's last query tile
+      int i = (t.end - st.row + T - 1) / T - 1;
+      for (; i < st.n && ok && keep != 0; i += st.n_tiles) {
+        const uint32_t stage = (slot + i) % S;
         for (int k = 0; k < 2 && ok; ++k) {
           ok = mbar_wait_warp(k == 0 ? &q_land[stage] : &o_land[stage], (landed >> stage) & 1u, ctl);
           if (!ok) break;
@@ -343,36 +374,47 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         }
         landed ^= 1u << stage;
       }
-      slot += n_tiles * group;
+      slot += st.n;
     }
   } else {
     // ---------------------------------------------------------------- elementwise
     const int quarter = (warp - 4) >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t rS = tS + lanes + 32 * quarter, rP = tP + lanes + 32 * quarter;
+    const uint32_t rP = tP + lanes + 32 * quarter;
+    // sums of part `part` of the steps: of dk (before the scale), of dv
+    auto part_of = [&](int part, int which) {
+      return p.partial + static_cast<size_t>(2 * part + which) * p.M * p.kv_heads * D;
+    };
     AttnScore<kCap, kBias> score(p);
     const float2 mul = both(score.mul);
     RingPos r;
     uint32_t turn = 0, step = 0;
     while (ok && items.advance()) {
       const AttnTileRef t = items.t;
-      const int hk = items.h;
       if (items.behind()) {
-        const int last = min(t.row0 + T, t.end);
-        attn_zero_rows<D>(p.dK, p.kv_heads, hk, t.row0, last, threadIdx.x - 128, 512);
-        attn_zero_rows<D>(p.dV, p.kv_heads, hk, t.row0, last, threadIdx.x - 128, 512);
+        const int last = min(t.row0 + T, t.end), i = threadIdx.x - 128;
+        const int hk = items.h / p.parts, part = items.h - hk * p.parts;
+        if (p.parts == 1) {
+          attn_zero_rows<D>(p.dK, p.kv_heads, hk, t.row0, last, i, 512);
+          attn_zero_rows<D>(p.dV, p.kv_heads, hk, t.row0, last, i, 512);
+        } else {             // as many bytes as twice the features in bf16
+          attn_zero_rows<2 * D>(reinterpret_cast<__nv_bfloat16*>(part_of(part, 0)), p.kv_heads, hk, t.row0, last, i, 512);
+          attn_zero_rows<2 * D>(reinterpret_cast<__nv_bfloat16*>(part_of(part, 1)), p.kv_heads, hk, t.row0, last, i, 512);
+        }
         continue;
       }
-      const int first = first_of(), n = (t.end - first + T - 1) / T * group;
+      const Steps sp = steps();
+      const int hk = sp.hk, first = sp.first, n = sp.n;
       const int key = t.row0 + (warp & 3) * 32 + lane;
       const bool all_keys = min(t.row0 + T, t.end) <= t.prefix_end;
-      int h = hk * group, tile0 = first;
-      score.head(p, h);
+      int h = sp.h, tile0 = sp.row;
+      if (n > 0) score.head(p, h);
       for (int i = 0; i < n && ok; ++i, ++step) {
         const int i0 = tile0 + 32 * quarter;                           // the first of this thread's 32 queries
-        ok = mbar_wait_warp(&st_full[r.stage], r.phase, ctl) && mbar_wait_warp(s_full, step & 1u, ctl);
+        ok = mbar_wait_warp(&st_full[r.stage], r.phase, ctl) && mbar_wait_warp(&s_full[step % NS], step / NS & 1u, ctl);
         if (!ok) break;
         tc_fence_after();
+        const uint32_t rS = tS + step % NS * T + lanes + 32 * quarter;
         const float* st = stat + r.stage * 2 * T + 32 * quarter;
         uint32_t v[1][32];
         float2 g[16];                     // p, then p d(cap tanh)
@@ -433,30 +475,54 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         tile0 += T;
         if (tile0 >= t.end && i + 1 < n) { tile0 = first; score.head(p, ++h); }
       }
-      ok = ok && mbar_wait_warp(acc_full, turn & 1u, ctl);
-      if (!ok) break;
-      ++turn;
-      tc_fence_after();
+      if (n > 0) {
+        ok = ok && mbar_wait_warp(acc_full, turn & 1u, ctl);
+        if (!ok) break;
+        ++turn;
+        tc_fence_after();
+      }
       // half of the warps store dk, half dv
       const bool is_k = quarter < 2;
       const int f0 = (quarter & 1) * (D / 2);
-      const float by = is_k ? p.scale : 1.0f;
-      uint4 w[D / 16];
-#pragma unroll
-      for (int c = 0; c < D / 2; c += 32) {
-        uint32_t o[32];
-        tmem_ld32((is_k ? tK : tV) + lanes + f0 + c, o);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) w[(c + e) / 8] = attn_pack8(&o[e], by);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty);
       const int key0 = key - lane;               // the warp's first
-      const size_t stride = static_cast<size_t>(p.kv_heads) * D * 2;
-      attn_store_rows<D / 16>(w, reinterpret_cast<uint8_t*>(is_k ? p.dK : p.dV) + key0 * stride +
-                                     (static_cast<size_t>(hk) * D + f0) * 2, stride, t.end - key0, lane);
+      const uint32_t acc = (is_k ? tK : tV) + lanes + f0;
+      if (p.parts == 1) {
+        const float by = is_k ? p.scale : 1.0f;
+        uint4 w[D / 16];
+#pragma unroll
+        for (int c = 0; c < D / 2; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(acc + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) w[(c + e) / 8] = attn_pack8(&o[e], by);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty);
+        const size_t stride = static_cast<size_t>(p.kv_heads) * D * 2;
+        attn_store_rows<D / 16>(w, reinterpret_cast<uint8_t*>(is_k ? p.dK : p.dV) + key0 * stride +
+                                       (static_cast<size_t>(hk) * D + f0) * 2, stride, t.end - key0, lane);
+      } else {
+        const size_t stride = static_cast<size_t>(p.kv_heads) * D * 4;
+        uint8_t* out = reinterpret_cast<uint8_t*>(part_of(sp.part, is_k ? 0 : 1)) + key0 * stride +
+                       (static_cast<size_t>(hk) * D + f0) * 4;
+#pragma unroll 1
+        for (int c = 0; c < D / 2; c += 32) {
+          uint32_t o[32] = {};
+          if (n > 0) {
+            tmem_ld32(acc + c, o);
+            tmem_wait_ld();
+          }
+          uint4 w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          attn_store_rows<8>(w, out + c * 4, stride, t.end - key0, lane);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (n > 0 && lane == 0) mbar_arrive(acc_empty);
+      }
     }
   }
 
@@ -466,6 +532,27 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
+}
+
+// dk and dv from the sums of their parts, added in order.  y: dk, dv.
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p) {
+  grid_dep_wait();
+  if (!attn_plan_ok(p) || p.plan.head[kPlanKv] == 0u) return;
+  const size_t n = static_cast<size_t>(p.M) * p.kv_heads * D;
+  const size_t i = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (i >= n) return;
+  const float* src = p.partial + blockIdx.y * n + i;
+  float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
+  for (int k = 1; k < p.parts; ++k) {
+    const float4 c = *reinterpret_cast<const float4*>(src + 2 * k * n), d = *reinterpret_cast<const float4*>(src + 2 * k * n + 4);
+    a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
+    b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
+  }
+  const float by = blockIdx.y == 0 ? p.scale : 1.0f;
+  *reinterpret_cast<uint4*>((blockIdx.y == 0 ? p.dK : p.dV) + i) =
+      make_uint4(pack_bf16x2(a.x * by, a.y * by), pack_bf16x2(a.z * by, a.w * by), pack_bf16x2(b.x * by, b.y * by),
+                 pack_bf16x2(b.z * by, b.w * by));
 }
 
 // ---------------------------------------------------------------------------

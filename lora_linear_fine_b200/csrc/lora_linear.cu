@@ -2301,6 +2301,21 @@ AttnParams attn_params(const lora_attn_desc* d, void* plan, const void* Q, const
   return p;
 }
 
+// Shares that the steps of a dk / dv item are cut into: as many as bring the
+// items to twice the SMs, but no more than 8 (nor than the query heads and
+// tiles of a document give steps for).
+int attn_bwd_parts(const lora_attn_desc* d) {
+  const int64_t tiles = ceil_div(d->M, kAttnTile), items = (tiles + d->n_docs) * d->kv_heads;
+  const int64_t steps = (d->heads / d->kv_heads) * ceil_div(d->M, kAttnTile * std::max<int64_t>(1, d->n_docs));
+  int parts = 1;
+  while (parts < 8 && items * parts < 2 * kTargetCtas && parts < steps) parts *= 2;
+  return parts;
+}
+
+size_t attn_stat_bytes(const lora_attn_desc* d) {
+  return align_up(static_cast<size_t>(d->M) * d->heads * 2 * sizeof(float), 256);
+}
+
 // Tensor map of one head-interleaved operand [M x heads * D]: tiles of kAttnTile rows x 64 features.
 bool attn_tm(CUtensorMap* tm, const void* ptr, const AttnParams& p, int heads, int D) {
   const uint64_t cols = static_cast<uint64_t>(heads) * D;
@@ -2343,9 +2358,15 @@ lora_status_t launch_attn_bwd(const AttnParams& p, int sms, cudaStream_t st) {
   launch_k(attn_delta_kernel<D>, dim3(static_cast<unsigned>(ceil_div(p.M, 32)), static_cast<unsigned>(ceil_div(p.heads, 8))),
            dim3(256), 0, st, false, p);
   LORA_TRY(check_launch("attn_delta_kernel"));
-  launch_k(kv, dim3(static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(p.plan.max_q) * p.kv_heads, sms))),
-           dim3(kAttnBwdThreads), AttnDkvCfg<D>::kSmemBytes, st, false, p, maps);
+  const int64_t kv_ctas = static_cast<int64_t>(p.plan.max_q) * p.kv_heads * p.parts;
+  launch_k(kv, dim3(static_cast<unsigned>(std::min<int64_t>(kv_ctas, sms))), dim3(kAttnBwdThreads),
+           AttnDkvCfg<D>::kSmemBytes, st, false, p, maps);
   LORA_TRY(check_launch("attn_dkv_kernel"));
+  if (p.parts > 1) {
+    launch_k(attn_join_kernel<D>, dim3(static_cast<unsigned>(ceil_div(static_cast<int64_t>(p.M) * p.kv_heads * D, 2048)), 2),
+             dim3(256), 0, st, false, p);
+    LORA_TRY(check_launch("attn_join_kernel"));
+  }
   launch_k(q, dim3(static_cast<unsigned>(std::min<int64_t>(ctas, sms))), dim3(kAttnBwdThreads), AttnDqCfg<D>::kSmemBytes,
            st, false, p, maps);
   return check_launch("attn_dq_kernel");
@@ -2516,7 +2537,9 @@ lora_status_t lora_linear_attn_fwd(const lora_attn_desc* d, void* plan, size_t p
 
 size_t lora_linear_attn_workspace_size(const lora_attn_desc* d) {
   if (check_attn_desc(d) != LORA_OK) return 0;
-  return kHeaderBytes + align_up(static_cast<size_t>(d->M) * d->heads * 2 * sizeof(float), 256);
+  const int parts = attn_bwd_parts(d);
+  return kHeaderBytes + attn_stat_bytes(d) +
+         (parts > 1 ? static_cast<size_t>(parts) * 2 * d->M * d->kv_heads * d->head_dim * sizeof(float) : 0);
 }
 
 lora_status_t lora_linear_attn_bwd(const lora_attn_desc* d, void* plan, size_t plan_bytes, const void* dO,
@@ -2543,6 +2566,8 @@ lora_status_t lora_linear_attn_bwd(const lora_attn_desc* d, void* plan, size_t p
   p.dK = static_cast<__nv_bfloat16*>(dK);
   p.dV = static_cast<__nv_bfloat16*>(dV);
   p.stat = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes + attn_stat_bytes(d));
+  p.parts = attn_bwd_parts(d);
   return d->head_dim == 64 ? launch_attn_bwd_mod<64>(p, dev.sms, static_cast<cudaStream_t>(stream))
                            : launch_attn_bwd_mod<128>(p, dev.sms, static_cast<cudaStream_t>(stream));
 }

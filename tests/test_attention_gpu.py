@@ -251,7 +251,9 @@ def test_long_document():
 
 
 def test_offsets_past_32_bits():
-    """Documents behind 2^31 elements of Q: the same bits as on their own."""
+    """Documents behind 2^31 elements of Q: the same as on their own (dK and dV
+    of the small batch are summed in parts: fp32 sums in another order, then one
+    rounding each, so at most one bf16 step, 2^-7, apart)."""
     import lora_linear_fine_b200 as L
     import torch
     H, Gk, D = 64, 8, 128
@@ -272,5 +274,7 @@ def test_offsets_past_32_bits():
     g = L.attention_backward(dO, Q, K, V, o, lse, plan, H, Gk)
     del dO
     g2 = L.attention_backward(small[0].clone(), *small, o2, lse2, p2, H, Gk)
-    for a, b in zip(g, g2):
-        assert torch.equal(a[-400:], b)
+    assert torch.equal(g[0][-400:], g2[0])
+    for a, b in zip(g[1:], g2[1:]):
+        a, b = a[-400:].float(), b.float()
+        assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 2.0 ** -16 * b.abs().max()).all()
