@@ -239,9 +239,9 @@ __device__ __forceinline__ float2 pair_of(const uint32_t* v) {
 }
 
 // 2^x of a pair on the FMA pipe: x = n + f with n whole and |f| <= 1/2 (adding
-// 1.5 * 2^23 leaves n in the low bits), 2^f by a polynomial of degree 4 with
-// the least largest relative error on that interval (2^-18.5), n added to the
-// exponent.  Below -126 the result is 2^-126.  The special function unit gives
+// 1.5 * 2^23 leaves n in the low bits), 2^f by a polynomial of degree 5 that is
+// 1 at 0 with the least largest relative error on that interval (2^-22.5 in
+// fp32), n added to the exponent.  Below -126 the result is 2^-126.  The special function unit gives
 // 16 exponentials a cycle and SM, fewer than a tile's products leave time for;
 // so the kernels form part of them this way.
 __device__ __forceinline__ float2 exp2_poly(float2 x) {
@@ -249,10 +249,11 @@ __device__ __forceinline__ float2 exp2_poly(float2 x) {
   x = make_float2(max_nan(x.x, -126.0f), max_nan(x.y, -126.0f));
   const float2 t = add2(x, both(kRound));
   const float2 f = fma2(add2(t, both(-kRound)), both(-1.0f), x);
-  float2 p = fma2(both(0.009570102207362652f), f, both(0.05591785907745361f));
-  p = fma2(p, f, both(0.240247443318367f));
-  p = fma2(p, f, both(0.6931217908859253f));
-  p = fma2(p, f, both(0.9999992847442627f));
+  float2 p = fma2(both(0.001326472731307149f), f, both(0.009671512991189957f));
+  p = fma2(p, f, both(0.05550733581185341f));
+  p = fma2(p, f, both(0.24022242426872253f));
+  p = fma2(p, f, both(0.6931470036506653f));
+  p = fma2(p, f, both(1.0f));
   return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
                      __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }

@@ -3,8 +3,12 @@
 // Three launches, none of which adds to another's sums, so the order of every
 // sum is fixed:
 //   attn_delta_kernel  delta_i = do_i . o_i, and the row statistics by head
-//   attn_dkv_kernel    a CTA a tile of 128 keys and a key / value head: dk, dv
-//   attn_dq_kernel     a CTA a tile of 128 queries and a query head: dq
+//   attn_dq_kernel     items of 128 queries and a query head: dq
+//   attn_dkv_kernel    items of 128 keys and a key / value head: dk, dv
+// delta from the rounded o is off by 2^-9 of |do| |o|, which is as much as dp -
+// delta itself for rows that see a few keys.  So attn_dq_kernel forms delta =
+// sum_j p_ij dp_ij in fp32 for the rows whose keys all lie in one tile, and
+// leaves it for attn_dkv_kernel; a row that sees one key has ds = 0 exactly.
 // The last two form p and ds each for itself: seven products a tile pair in
 // place of five, against adding dq tiles into memory from every key tile,
 // whose order would change from call to call and whose 64 KB a tile pair in
@@ -452,6 +456,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             attn_publish(&p_full[e0 / (32 / kParts)], lane);
           }
         }
+        // the first row of a document without a longer prefix sees one key
+        if (key == t.begin && i0 == t.begin && t.prefix_end <= t.begin + 1) g[0].x = 0.0f;
         ok = mbar_wait_warp(dp_full, step & 1u, ctl);
         if (!ok) break;
         tc_fence_after();
@@ -569,7 +575,7 @@ struct AttnDqCfg {
   static constexpr int kTileBytes = kAttnTile * D * 2;
   static constexpr int kStagesK = D == 128 ? 3 : 4, kStagesV = D == 128 ? 2 : 4;
   static constexpr int kBars = 3 * kStagesK + 3 * kStagesV + 2 + 2 + 1 + 1 + 2 + 1;
-  static constexpr int kSmemBytes = (2 + kStagesK + kStagesV) * kTileBytes + kBars * 8 + 16 + 1024;
+  static constexpr int kSmemBytes = (2 + kStagesK + kStagesV) * kTileBytes + 3 * kAttnTile * 4 + kBars * 8 + 16 + 1024;
   static_assert(kSmemBytes <= kSmemLimitBytes, "shared memory");
 };
 
@@ -584,7 +590,8 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
   uint8_t* so = sq + C::kTileBytes;
   uint8_t* ring_k = so + C::kTileBytes;
   uint8_t* ring_v = ring_k + SK * C::kTileBytes;
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(ring_v + SV * C::kTileBytes);
+  float* share = reinterpret_cast<float*>(ring_v + SV * C::kTileBytes);      // [3][T]
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(share + 3 * T);
   uint64_t* k_empty = k_full + SK;
   uint64_t* v_full = k_empty + SK;
   uint64_t* v_empty = v_full + SV;
@@ -787,33 +794,69 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       const int see = min(max(row + 1, t.prefix_end), t.end);              // keys [begin, see)
       const int all = min(max(t.row0 + 1, t.prefix_end), t.end);           // ... that every row sees
       const float nlse = mine ? p.stat[static_cast<size_t>(h) * p.M + row] : -INFINITY;
-      const float ndelta = mine ? p.stat[static_cast<size_t>(p.heads + h) * p.M + row] : 0.0f;
+      float ndelta = mine ? p.stat[static_cast<size_t>(p.heads + h) * p.M + row] : 0.0f;
       score.head(p, h);
       const float2 shift = both(nlse);
+      const bool lone = see - t.begin == 1;
+      uint32_t v[1][32];
+      // p of 32 keys from the products in v
+      auto probabilities = [&](float2 (&y)[16], float2 (&dt)[16], int j0) {
+        score.template values<1, true>(v, dt);
+        const float d0 = static_cast<float>(j0 - row);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+          y[e / 2] = attn_exp2<AttnScore<kCap, kBias>::kPoly>(
+              fma2(pair_of(&v[0][e]), mul, score.shifted(shift, d0, e, 1.0f)), e / 2);
+        if (j0 + 32 > all) {
+          const int lim = see - j0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (2 * i >= lim) y[i].x = 0.0f;
+            if (2 * i + 1 >= lim) y[i].y = 0.0f;
+          }
+        }
+      };
+      if (n == 1) {
+        // delta = sum_j p_ij dp_ij over the four warps of a row
+        float2 sum = make_float2(0.0f, 0.0f);
+        ok = mbar_wait_warp(&s_full[step & 1u], (step >> 1) & 1u, ctl) && mbar_wait_warp(dp_full, step & 1u, ctl);
+        if (ok) {
+          tc_fence_after();
+          float2 y[16], dt[16];
+          tmem_ld32(tS + (step & 1u) * T + lanes + 32 * quarter, v[0]);
+          tmem_wait_ld();
+          probabilities(y, dt, t.begin + 32 * quarter);
+          tmem_ld32(rP, v[0]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) sum = fma2(y[e / 2], pair_of(&v[0][e]), sum);
+        }
+        const int r = (warp & 3) * 32 + lane;
+        if (quarter > 0) share[(quarter - 1) * T + r] = sum.x + sum.y;
+        ok = bar_sync_and<512>(1, ok);
+        if (!ok) break;
+        if (quarter == 0) {
+          ndelta = -(((sum.x + sum.y) + share[r]) + (share[T + r] + share[2 * T + r]));
+          share[r] = ndelta;
+          if (mine) p.stat[static_cast<size_t>(p.heads + h) * p.M + row] = ndelta;
+        }
+        ok = bar_sync_and<512>(1, ok);
+        ndelta = share[r];
+      }
       for (int j = 0; j < n && ok; ++j, ++step) {
         const int j0 = t.begin + j * T + 32 * quarter;                     // the first of this thread's 32 keys
         const uint32_t rS = tS + (step & 1u) * T + lanes + 32 * quarter;
         ok = mbar_wait_warp(&s_full[step & 1u], (step >> 1) & 1u, ctl);
         if (!ok) break;
         tc_fence_after();
-        uint32_t v[1][32];
-        float2 g[16];                     // p d(cap tanh)
+        float2 g[16], dt[16];             // g: p d(cap tanh)
         tmem_ld32(rS, v[0]);
         tmem_wait_ld();
-        score.template values<1, true>(v, g);
-        const float d0 = static_cast<float>(j0 - row);
+        probabilities(g, dt, j0);
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float2 y = attn_exp2<AttnScore<kCap, kBias>::kPoly>(fma2(pair_of(&v[0][e]), mul, score.shifted(shift, d0, e, 1.0f)), e / 2);
-          g[e / 2] = kCap ? mul2(y, g[e / 2]) : y;
-        }
-        if (j0 + 32 > all) {
-          const int lim = see - j0;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (2 * i >= lim) g[i].x = 0.0f;
-            if (2 * i + 1 >= lim) g[i].y = 0.0f;
-          }
+        for (int i = 0; i < 16; ++i) {
+          if constexpr (kCap) g[i] = mul2(g[i], dt[i]);
+          if (lone) g[i] = make_float2(0.0f, 0.0f);
         }
         ok = mbar_wait_warp(dp_full, step & 1u, ctl);
         if (!ok) break;

@@ -2358,6 +2358,9 @@ lora_status_t launch_attn_bwd(const AttnParams& p, int sms, cudaStream_t st) {
   launch_k(attn_delta_kernel<D>, dim3(static_cast<unsigned>(ceil_div(p.M, 32)), static_cast<unsigned>(ceil_div(p.heads, 8))),
            dim3(256), 0, st, false, p);
   LORA_TRY(check_launch("attn_delta_kernel"));
+  launch_k(q, dim3(static_cast<unsigned>(std::min<int64_t>(ctas, sms))), dim3(kAttnBwdThreads), AttnDqCfg<D>::kSmemBytes,
+           st, false, p, maps);
+  LORA_TRY(check_launch("attn_dq_kernel"));
   const int64_t kv_ctas = static_cast<int64_t>(p.plan.max_q) * p.kv_heads * p.parts;
   launch_k(kv, dim3(static_cast<unsigned>(std::min<int64_t>(kv_ctas, sms))), dim3(kAttnBwdThreads),
            AttnDkvCfg<D>::kSmemBytes, st, false, p, maps);
@@ -2367,9 +2370,7 @@ lora_status_t launch_attn_bwd(const AttnParams& p, int sms, cudaStream_t st) {
              dim3(256), 0, st, false, p);
     LORA_TRY(check_launch("attn_join_kernel"));
   }
-  launch_k(q, dim3(static_cast<unsigned>(std::min<int64_t>(ctas, sms))), dim3(kAttnBwdThreads), AttnDqCfg<D>::kSmemBytes,
-           st, false, p, maps);
-  return check_launch("attn_dq_kernel");
+  return LORA_OK;
 }
 
 template <int D>

@@ -103,6 +103,40 @@ def test_prefix_with_bias_and_cap(D):
     _check([300, 150], 0, 2, 2, D, prefix=[133, 150], slopes=[0.25, 0.03], cap=8.0, seed=11)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("cap", [0.0, 7.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_that_see_one_key(D, cap, causal):
+    """The softmax of one score does not depend on it: dQ is zero exactly, and so
+    is dK of a document of one row; lse is the score."""
+    lens = [1, 1, 5, 1, 130, 1]
+    out, (Q, K, V, dO), _, _ = _run(lens, 2, 4, 2, D, cap=cap, causal=causal, seed=19)
+    one = [0, 1, 7, 138]
+    first = [2, 8]
+    assert not out["dQ"][one + (first if causal else [])].any() and not out["dK"][one].any()
+    z = (Q[one].double().view(4, 4, D) * K[one].double().view(4, 2, D).repeat_interleave(2, 1)).sum(-1) * D ** -0.5
+    z = cap * np.tanh(G.host_f64(z) / cap) if cap else G.host_f64(z)
+    # a handful of fp32 roundings of a sum of D terms of a few units
+    assert np.abs(G.host_f64(out["lse"][one]) - z).max() <= 2.0 ** -20 * (4 + np.abs(z).max())
+    # p is 1 where the reference is the row's maximum.  Under a cap it is not, and
+    # p / l = 1 with p rounded to bf16 (half a step, 2^-8) times V is rounded once
+    # more: (1 + 2^-8)^2 - 1 <= 2^-7 (1 + 2^-9)
+    got, want = (G.host_f64(t) for t in (out["O"][one].view(4, 4, D), V[one].view(4, 2, D).repeat_interleave(2, 1)))
+    assert (np.abs(got - want) <= (2.0 ** -7 * (1 + 2.0 ** -9) if cap else 0.0) * np.abs(want)).all()
+
+
+def test_gradients_of_short_documents():
+    """Rows with a few keys: delta is not the one of the rounded O, so dQ and dK
+    stay within the roundings of ds (2^-9 rms each) and of the output."""
+    import torch
+    lens = [2] * 9 + [3] * 7 + [4, 7, 11]
+    out, (Q, K, V, dO), _, _ = _run(lens, 0, 4, 2, 128, cap=20.0, seed=20)
+    ref = O.attention(*(G.host_f64(t) for t in (Q, K, V)), _starts(lens), 4, 2, softcap=20.0, dO=G.host_f64(dO))
+    for name in ("dQ", "dK", "dV"):
+        off = np.linalg.norm(G.host_f64(out[name]) - ref[name]) / np.linalg.norm(ref[name])
+        assert off <= 2.0 ** -8, f"{name}: {off:.3g}"
+
+
 def test_scale_and_large_scores():
     """Scores of a few tens, where one key takes almost all of a row."""
     _check([260, 100], 0, 2, 1, 64, scale=0.02, seed=12)
