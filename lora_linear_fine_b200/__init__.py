@@ -648,16 +648,14 @@ def _refuse(what):
 def _tensors(device, *named):
     """Checks (name, tensor or None, dtype, shape): device, type, shape, density.  A dimension of None is any."""
     for name, t, dtype, shape in named:
-        if t is None:
-            continue
-        if t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous():
+        if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
             continue
         if t.device != device:
             _refuse(f"{name} is on {t.device}, not {device}")
         if t.dtype != dtype:
             _refuse(f"{name} is {t.dtype}, not {dtype}")
         if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-            _refuse(f"{name} has shape {tuple(t.shape)}, not {shape}")
+            _refuse(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
         if not t.is_contiguous():
             _refuse(f"{name} is not contiguous")
 
@@ -667,30 +665,35 @@ class _On:
     current stream) as the current ones, so that outputs belong to the stream
     that writes them; the inputs are recorded on a stream of the caller's."""
 
-    __slots__ = ("_ctx", "_handle")
-
     def __init__(self, device, stream, *inputs):
         import torch
         if device.type != "cuda":
             _refuse(f"the tensors are on {device}, not on a CUDA device")
         if stream is None:
-            self._ctx = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-            self._handle = torch._C._cuda_getCurrentRawStream(device.index)
+            self._ctx = torch.cuda.device(device)
             return
         if stream.device != device:
             _refuse(f"the stream is on {stream.device}, not {device}")
         for t in inputs:
             if t is not None:
                 t.record_stream(stream)
-        self._ctx, self._handle = torch.cuda.stream(stream), stream.cuda_stream
+        self._ctx = torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self._handle
+        self._ctx.__enter__()
+        return _stream_handle()
 
     def __exit__(self, *exc):
-        return None if self._ctx is None else self._ctx.__exit__(*exc)
+        return self._ctx.__exit__(*exc)
+
+
+def _call(run, device, stream, *inputs):
+    """run(stream handle) with the device and the stream of a call as the current ones."""
+    import torch
+    if stream is None and device.type == "cuda" and torch.cuda.current_device() == device.index:
+        return run(torch._C._cuda_getCurrentRawStream(device.index))      # they are
+    with _On(device, stream, *inputs) as st:
+        return run(st)
 
 
 def _workspace(workspace, nbytes, device):
@@ -709,14 +712,17 @@ def layer_norm(X, g, b=None, eps=1e-5, stream=None):
     if X.dim() != 2:
         _refuse(f"X has shape {tuple(X.shape)}")
     M, d = X.shape
-    bf16, f32 = torch.bfloat16, torch.float32
-    _tensors(X.device, ("X", X, bf16, (M, d)), ("g", g, bf16, (d,)), ("b", b, bf16, (d,)))
-    with _On(X.device, stream, X, g, b) as st:
+    bf16, device = torch.bfloat16, X.device
+    _tensors(device, ("X", X, bf16, X.shape), ("g", g, bf16, (d,)), ("b", b, bf16, (d,)))
+
+    def run(st):
         Y = torch.empty_like(X)
-        mean, rstd = (torch.empty(M, dtype=f32, device=X.device) for _ in range(2))
-        _check(lora_linear_layernorm_fwd(_ptr(X), _ptr(g), _ptr(b), M, d, eps, _ptr(Y), _ptr(mean), _ptr(rstd), st),
-               "lora_linear_layernorm_fwd")
-    return Y, mean, rstd
+        mean = torch.empty(M, dtype=torch.float32, device=device)
+        rstd = torch.empty_like(mean)
+        _check(_lib.lora_linear_layernorm_fwd(X.data_ptr(), g.data_ptr(), _ptr(b), M, d, eps, Y.data_ptr(),
+                                              mean.data_ptr(), rstd.data_ptr(), st), "lora_linear_layernorm_fwd")
+        return Y, mean, rstd
+    return _call(run, device, stream, X, g, b)
 
 
 def layer_norm_backward(dY, X, g, mean, rstd, bias=True, workspace=None, stream=None):
@@ -726,20 +732,22 @@ def layer_norm_backward(dY, X, g, mean, rstd, bias=True, workspace=None, stream=
     if X.dim() != 2:
         _refuse(f"X has shape {tuple(X.shape)}")
     M, d = X.shape
-    bf16, f32 = torch.bfloat16, torch.float32
+    bf16, f32, device = torch.bfloat16, torch.float32, X.device
     if dY.dtype not in (bf16, f32):
         _refuse(f"dY is {dY.dtype}, not bfloat16 or float32")
-    _tensors(X.device, ("dY", dY, dY.dtype, (M, d)), ("X", X, bf16, (M, d)), ("g", g, bf16, (d,)),
+    _tensors(device, ("dY", dY, dY.dtype, X.shape), ("X", X, bf16, X.shape), ("g", g, bf16, (d,)),
              ("mean", mean, f32, (M,)), ("rstd", rstd, f32, (M,)))
-    with _On(X.device, stream, dY, X, g, mean, rstd) as st:
+
+    def run(st):
         dX = torch.empty_like(X)
-        dg = torch.empty(d, dtype=f32, device=X.device)
-        db = torch.empty(d, dtype=f32, device=X.device) if bias else None
-        ws = _workspace(workspace, lora_linear_layernorm_workspace_size(M, d), X.device)
-        _check(lora_linear_layernorm_bwd(_ptr(dY), dY.dtype == f32, _ptr(X), _ptr(g), _ptr(mean), _ptr(rstd), M, d,
-                                         _ptr(dX), _ptr(dg), _ptr(db), ws.buf.data_ptr(), ws.nbytes, st),
-               "lora_linear_layernorm_bwd")
-    return dX, dg, db
+        dg = torch.empty(d, dtype=f32, device=device)
+        db = torch.empty_like(dg) if bias else None
+        ws = _workspace(workspace, lora_linear_layernorm_workspace_size(M, d), device)
+        _check(_lib.lora_linear_layernorm_bwd(dY.data_ptr(), dY.dtype == f32, X.data_ptr(), g.data_ptr(),
+                                              mean.data_ptr(), rstd.data_ptr(), M, d, dX.data_ptr(), dg.data_ptr(),
+                                              _ptr(db), ws.buf.data_ptr(), ws.nbytes, st), "lora_linear_layernorm_bwd")
+        return dX, dg, db
+    return _call(run, device, stream, dY, X, g, mean, rstd)
 
 
 def rotary_tables(n_pos, rot, base=10000.0, scaling="none", factor=1.0, low=1.0, high=4.0, original=8192,
@@ -758,10 +766,13 @@ def rotary_tables(n_pos, rot, base=10000.0, scaling="none", factor=1.0, low=1.0,
     if device.type == "cuda" and device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
     desc = make_rotary_table_desc(n_pos, rot, base, scaling, factor, low, high, original, amplitude)
-    with _On(device, stream) as st:
-        cos, sin = (torch.empty((n_pos, rot // 2), dtype=torch.float32, device=device) for _ in range(2))
-        _check(lora_linear_rotary_tables(desc, _ptr(cos), _ptr(sin), st), "lora_linear_rotary_tables")
-    return cos, sin
+
+    def run(st):
+        cos = torch.empty((n_pos, rot // 2), dtype=torch.float32, device=device)
+        sin = torch.empty_like(cos)
+        _check(lora_linear_rotary_tables(desc, cos.data_ptr(), sin.data_ptr(), st), "lora_linear_rotary_tables")
+        return cos, sin
+    return _call(run, device, stream)
 
 
 def rotary(Q, K, pos, cos, sin, head_dim, layout="half", inverse=False, inplace=False, workspace=None, stream=None):
@@ -774,24 +785,27 @@ def rotary(Q, K, pos, cos, sin, head_dim, layout="half", inverse=False, inplace=
         _refuse(f"layout {layout!r} is none of {sorted(ROTARY_LAYOUTS)}")
     if Q.dim() != 2 or cos.dim() != 2:
         _refuse(f"Q has shape {tuple(Q.shape)}, cos {tuple(cos.shape)}")
-    M, n_pos, rot = Q.shape[0], cos.shape[0], 2 * cos.shape[1]
-    if head_dim <= 0 or Q.shape[1] % head_dim != 0:
-        _refuse(f"{Q.shape[1]} features are no heads of {head_dim}")
+    (M, q_cols), (n_pos, half) = Q.shape, cos.shape
+    if head_dim <= 0 or q_cols % head_dim != 0:
+        _refuse(f"{q_cols} features are no heads of {head_dim}")
     if K is not None and (K.dim() != 2 or K.shape[1] % head_dim != 0):
         _refuse(f"K's features are no heads of {head_dim}")
-    bf16, f32 = torch.bfloat16, torch.float32
-    _tensors(Q.device, ("Q", Q, bf16, Q.shape), ("K", K, bf16, (M, None if K is None else K.shape[1])),
-             ("pos", pos, torch.int32, (M,)), ("cos", cos, f32, cos.shape), ("sin", sin, f32, cos.shape))
-    desc = make_rotary_desc(M, Q.shape[1] // head_dim, 0 if K is None else K.shape[1] // head_dim, head_dim, rot,
-                            layout, inverse)
-    rope = make_rope_desc(_ptr(pos), _ptr(cos), _ptr(sin), n_pos, head_dim)
-    with _On(Q.device, stream, Q, K, pos, cos, sin) as st:
+    k_cols = 0 if K is None else K.shape[1]
+    bf16, f32, device = torch.bfloat16, torch.float32, Q.device
+    _tensors(device, ("Q", Q, bf16, Q.shape), ("K", K, bf16, (M, k_cols)), ("pos", pos, torch.int32, (M,)),
+             ("cos", cos, f32, cos.shape), ("sin", sin, f32, cos.shape))
+
+    def run(st):
         Yq = Q if inplace else torch.empty_like(Q)
         Yk = K if inplace or K is None else torch.empty_like(K)
-        ws = _workspace(workspace, 256, Q.device)
-        _check(lora_linear_rotary(desc, rope, _ptr(Q), _ptr(K), _ptr(Yq), _ptr(Yk), ws.buf.data_ptr(), ws.nbytes, st),
-               "lora_linear_rotary")
-    return Yq, Yk
+        ws = _workspace(workspace, 256, device)
+        desc = LoraRotaryDesc(M, q_cols // head_dim, k_cols // head_dim, head_dim, 2 * half, ROTARY_LAYOUTS[layout],
+                              bool(inverse))
+        rope = LoraRopeDesc(pos.data_ptr(), cos.data_ptr(), sin.data_ptr(), n_pos, head_dim)
+        _check(_lib.lora_linear_rotary(desc, rope, Q.data_ptr(), _ptr(K), Yq.data_ptr(), _ptr(Yk), ws.buf.data_ptr(),
+                                       ws.nbytes, st), "lora_linear_rotary")
+        return Yq, Yk
+    return _call(run, device, stream, Q, K, pos, cos, sin)
 
 
 class AttentionPlan:
@@ -811,10 +825,13 @@ class AttentionPlan:
         self.M, self.n_docs, self.causal, self.nbytes = int(M), n, bool(causal), lora_linear_attn_plan_size(M, n)
         if self.nbytes <= 0:
             _refuse(f"{M} rows in {n} documents")
-        with _On(starts.device, stream, starts, prefix_len) as st:
-            self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=starts.device)
-            _check(lora_linear_attn_plan(_ptr(starts), _ptr(prefix_len), self.M, n, self.causal, self.buf.data_ptr(),
-                                         self.nbytes, st), "lora_linear_attn_plan")
+
+        def run(st):
+            buf = torch.empty(self.nbytes, dtype=torch.uint8, device=starts.device)
+            _check(_lib.lora_linear_attn_plan(starts.data_ptr(), _ptr(prefix_len), self.M, n, self.causal,
+                                              buf.data_ptr(), self.nbytes, st), "lora_linear_attn_plan")
+            return buf
+        self.buf = _call(run, starts.device, stream, starts, prefix_len)
 
     def status(self, stream=None):
         return lora_linear_device_status(self.buf.data_ptr(), _stream_handle(stream))[1]
@@ -824,13 +841,14 @@ def _attention_args(Q, K, V, plan, heads, kv_heads, scale, softcap, slopes):
     import torch
     if Q.dim() != 2 or heads <= 0 or kv_heads <= 0 or Q.shape[1] % heads != 0:
         _refuse(f"Q has shape {tuple(Q.shape)} for {heads} heads")
-    M, D, bf16 = Q.shape[0], Q.shape[1] // heads, torch.bfloat16
+    M, cols = Q.shape
+    D, bf16 = cols // heads, torch.bfloat16
     if M != plan.M:
         _refuse(f"{M} rows with a plan of {plan.M}")
-    _tensors(Q.device, ("Q", Q, bf16, (M, heads * D)), ("K", K, bf16, (M, kv_heads * D)),
-             ("V", V, bf16, (M, kv_heads * D)), ("slopes", slopes, torch.float32, (heads,)),
-             ("the plan", plan.buf, torch.uint8, (plan.nbytes,)))
-    return make_attn_desc(M, plan.n_docs, heads, kv_heads, D, plan.causal, scale, softcap)
+    kv = (M, kv_heads * D)
+    _tensors(Q.device, ("Q", Q, bf16, Q.shape), ("K", K, bf16, kv), ("V", V, bf16, kv),
+             ("slopes", slopes, torch.float32, (heads,)), ("the plan", plan.buf, torch.uint8, (plan.nbytes,)))
+    return LoraAttnDesc(M, plan.n_docs, heads, kv_heads, D, plan.causal, D ** -0.5 if scale is None else scale, softcap)
 
 
 def attention(Q, K, V, plan, heads, kv_heads, scale=None, softcap=0.0, slopes=None, stream=None):
@@ -841,12 +859,16 @@ def attention(Q, K, V, plan, heads, kv_heads, scale=None, softcap=0.0, slopes=No
     input."""
     import torch
     desc = _attention_args(Q, K, V, plan, heads, kv_heads, scale, softcap, slopes)
-    with _On(Q.device, stream, Q, K, V, slopes, plan.buf) as st:
+    device = Q.device
+
+    def run(st):
         O = torch.empty_like(Q)
-        lse = torch.empty((Q.shape[0], heads), dtype=torch.float32, device=Q.device)
-        _check(lora_linear_attn_fwd(desc, plan.buf.data_ptr(), plan.nbytes, _ptr(Q), _ptr(K), _ptr(V), _ptr(slopes),
-                                    _ptr(O), _ptr(lse), st), "lora_linear_attn_fwd")
-    return O, lse
+        lse = torch.empty((plan.M, heads), dtype=torch.float32, device=device)
+        _check(_lib.lora_linear_attn_fwd(desc, plan.buf.data_ptr(), plan.nbytes, Q.data_ptr(), K.data_ptr(),
+                                         V.data_ptr(), _ptr(slopes), O.data_ptr(), lse.data_ptr(), st),
+               "lora_linear_attn_fwd")
+        return O, lse
+    return _call(run, device, stream, Q, K, V, slopes, plan.buf)
 
 
 def attention_backward(dO, Q, K, V, O, lse, plan, heads, kv_heads, scale=None, softcap=0.0, slopes=None,
@@ -854,12 +876,16 @@ def attention_backward(dO, Q, K, V, O, lse, plan, heads, kv_heads, scale=None, s
     """(dQ, dK, dV) of ``attention`` for its O and lse."""
     import torch
     desc = _attention_args(Q, K, V, plan, heads, kv_heads, scale, softcap, slopes)
-    _tensors(Q.device, ("dO", dO, torch.bfloat16, Q.shape), ("O", O, torch.bfloat16, Q.shape),
+    device = Q.device
+    _tensors(device, ("dO", dO, torch.bfloat16, Q.shape), ("O", O, torch.bfloat16, Q.shape),
              ("lse", lse, torch.float32, (plan.M, heads)))
-    with _On(Q.device, stream, dO, Q, K, V, O, lse, slopes, plan.buf) as st:
+
+    def run(st):
         dQ, dK, dV = torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V)
-        ws = _workspace(workspace, lora_linear_attn_workspace_size(desc), Q.device)
-        _check(lora_linear_attn_bwd(desc, plan.buf.data_ptr(), plan.nbytes, _ptr(dO), _ptr(Q), _ptr(K), _ptr(V),
-                                    _ptr(O), _ptr(lse), _ptr(slopes), _ptr(dQ), _ptr(dK), _ptr(dV),
-                                    ws.buf.data_ptr(), ws.nbytes, st), "lora_linear_attn_bwd")
-    return dQ, dK, dV
+        ws = _workspace(workspace, _lib.lora_linear_attn_workspace_size(desc), device)
+        _check(_lib.lora_linear_attn_bwd(desc, plan.buf.data_ptr(), plan.nbytes, dO.data_ptr(), Q.data_ptr(),
+                                         K.data_ptr(), V.data_ptr(), O.data_ptr(), lse.data_ptr(), _ptr(slopes),
+                                         dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.buf.data_ptr(), ws.nbytes, st),
+               "lora_linear_attn_bwd")
+        return dQ, dK, dV
+    return _call(run, device, stream, dO, Q, K, V, O, lse, slopes, plan.buf)
