@@ -1,18 +1,19 @@
 // lora_attention_bwd.cuh — the attention backward on the tensor cores.
 //
-// Three launches, none of which adds to another's sums, so the order of every
+// Two kernels, neither of which adds to another's sums, so the order of every
 // sum is fixed:
-//   attn_delta_kernel  delta_i = do_i . o_i, and the row statistics by head
-//   attn_dq_kernel     items of 128 queries and a query head: dq
+//   attn_dq_kernel     items of 128 queries and a query head: delta, dq
 //   attn_dkv_kernel    items of 128 keys and a key / value head: dk, dv
-// delta from the rounded o is off by 2^-9 of |do| |o|, which is as much as dp -
-// delta itself for rows that see a few keys.  So attn_dq_kernel forms delta =
-// sum_j p_ij dp_ij in fp32 for the rows whose keys all lie in one tile, and
-// leaves it for attn_dkv_kernel; a row that sees one key has ds = 0 exactly.
-// The last two form p and ds each for itself: seven products a tile pair in
-// place of five, against adding dq tiles into memory from every key tile,
-// whose order would change from call to call and whose 64 KB a tile pair in
-// fp32 would be more traffic than the two products take time.
+// Each forms p and ds for itself: seven products a tile pair in place of five,
+// against adding dq tiles into memory from every key tile, whose order would
+// change from call to call and whose 64 KB a tile pair in fp32 would be more
+// traffic than the two products take time.
+//
+// delta_i = do_i . o_i comes from the rounded o, off by 2^-9 of |do| |o|, which
+// is as much as dp - delta itself for rows that see a few keys.  So for rows
+// whose keys all lie in one tile it is sum_j p_ij dp_ij in fp32, and a row that
+// sees one key has ds = 0 exactly.  attn_dq_kernel leaves delta and lse by head
+// for attn_dkv_kernel.
 #pragma once
 
 #include "lora_attention.cuh"
@@ -24,43 +25,6 @@ constexpr int kAttnBwdThreads = 640;     // warps: TMA, MMA, statistics, trimmin
 struct AttnBwdMaps {
   CUtensorMap q, k, v, d_o;   // [M x heads * D] bf16, box 64 x 128, 128-byte swizzle
 };
-
-// ---------------------------------------------------------------------------
-// delta
-// ---------------------------------------------------------------------------
-// stat[0][h][m] = -lse_mh log2(e), stat[1][h][m] = -delta_mh.  A CTA takes 32
-// rows of 8 heads; the results pass through shared memory so that both sides
-// move whole sectors.
-template <int D>
-__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int kLanes = D / 8, kPer = 256 / kLanes;      // threads a row and head; pairs of them at a time
-  __shared__ float s[8][33];
-  grid_dep_wait();
-  const int m0 = blockIdx.x * 32, h0 = blockIdx.y * 8;
-  const int lane = threadIdx.x % kLanes;
-#pragma unroll
-  for (int k = 0; k < 256 / kPer; ++k) {
-    const int pair = k * kPer + threadIdx.x / kLanes;
-    const int m = m0 + pair / 8, h = h0 + pair % 8;
-    float d = 0.0f;
-    if (m < p.M && h < p.heads) {
-      const size_t at = (static_cast<size_t>(m) * p.heads + h) * D + 8 * lane;
-      float a[8], b[8];
-      unpack_bf16x8(*reinterpret_cast<const uint4*>(p.dO + at), a);
-      unpack_bf16x8(*reinterpret_cast<const uint4*>(p.O + at), b);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) d = fmaf(a[e], b[e], d);
-    }
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (lane == 0) s[pair % 8][pair / 8] = d;
-  }
-  __syncthreads();
-  const int m = m0 + (threadIdx.x & 31), h = h0 + (threadIdx.x >> 5);
-  if (m >= p.M || h >= p.heads) return;
-  p.stat[static_cast<size_t>(h) * p.M + m] = -p.lse[static_cast<size_t>(m) * p.heads + h] * kLog2e;
-  p.stat[static_cast<size_t>(p.heads + h) * p.M + m] = -s[threadIdx.x >> 5][threadIdx.x & 31];
-}
 
 // Part c of a thread's 32 packed values over its first columns.
 template <int kParts>
@@ -564,6 +528,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 // ---------------------------------------------------------------------------
 // dq
 // ---------------------------------------------------------------------------
+// stat[0][h][m] = -lse_mh log2(e), stat[1][h][m] = -delta_mh are written here.
 // For each key tile j that the queries see:
 //   S = Q K_j^T, dP = dO V_j^T,  dS = exp2(S - lse) (dP - delta),  dQ += dS K_j
 // S has two buffers (dS is written over the one it came from), so the products
@@ -793,8 +758,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       const bool mine = row < t.end;
       const int see = min(max(row + 1, t.prefix_end), t.end);              // keys [begin, see)
       const int all = min(max(t.row0 + 1, t.prefix_end), t.end);           // ... that every row sees
-      const float nlse = mine ? p.stat[static_cast<size_t>(h) * p.M + row] : -INFINITY;
-      float ndelta = mine ? p.stat[static_cast<size_t>(p.heads + h) * p.M + row] : 0.0f;
+      const float nlse = mine ? -p.lse[static_cast<size_t>(row) * p.heads + h] * kLog2e : -INFINITY;
       score.head(p, h);
       const float2 shift = both(nlse);
       const bool lone = see - t.begin == 1;
@@ -816,33 +780,66 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
           }
         }
       };
+      // delta: a quarter of the row's terms here
+      float sum = 0.0f;
       if (n == 1) {
-        // delta = sum_j p_ij dp_ij over the four warps of a row
-        float2 sum = make_float2(0.0f, 0.0f);
+        // sum_j p_ij dp_ij
         ok = mbar_wait_warp(&s_full[step & 1u], (step >> 1) & 1u, ctl) && mbar_wait_warp(dp_full, step & 1u, ctl);
         if (ok) {
           tc_fence_after();
-          float2 y[16], dt[16];
+          float2 y[16], dt[16], two = make_float2(0.0f, 0.0f);
           tmem_ld32(tS + (step & 1u) * T + lanes + 32 * quarter, v[0]);
           tmem_wait_ld();
           probabilities(y, dt, t.begin + 32 * quarter);
           tmem_ld32(rP, v[0]);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) sum = fma2(y[e / 2], pair_of(&v[0][e]), sum);
+          for (int e = 0; e < 32; e += 2) two = fma2(y[e / 2], pair_of(&v[0][e]), two);
+          sum = two.x + two.y;
         }
-        const int r = (warp & 3) * 32 + lane;
-        if (quarter > 0) share[(quarter - 1) * T + r] = sum.x + sum.y;
-        ok = bar_sync_and<512>(1, ok);
-        if (!ok) break;
-        if (quarter == 0) {
-          ndelta = -(((sum.x + sum.y) + share[r]) + (share[T + r] + share[2 * T + r]));
-          share[r] = ndelta;
-          if (mine) p.stat[static_cast<size_t>(p.heads + h) * p.M + row] = ndelta;
+      } else {
+        // do_i . o_i: kL lanes a row, so that whole pieces of rows are read;
+        // dO lies in shared memory until the item's second step at least
+        constexpr int kL = D / 32;
+        const int first = lane / kL * kL, chunk = quarter * kL + lane % kL, r0 = (warp & 3) * 32;
+        uint4 o[kL];
+#pragma unroll
+        for (int i = 0; i < kL; ++i) {
+          const int m = min(t.row0 + r0 + first + i, t.end - 1);
+          o[i] = __ldg(reinterpret_cast<const uint4*>(p.O + (static_cast<size_t>(m) * p.heads + h) * D) + chunk);
         }
-        ok = bar_sync_and<512>(1, ok);
-        ndelta = share[r];
+        ok = mbar_wait_warp(qo_full, turn & 1u, ctl);
+        if (ok) {
+#pragma unroll
+          for (int i = 0; i < kL; ++i) {
+            const int r = r0 + first + i;
+            const uint4 g = *reinterpret_cast<const uint4*>(so + (chunk / 8) * (T * 128) + r * 128 + ((chunk % 8) ^ (r & 7)) * 16);
+            float2 two = mul2(unpack_bf16x2(o[i].x), unpack_bf16x2(g.x));
+            two = fma2(unpack_bf16x2(o[i].y), unpack_bf16x2(g.y), two);
+            two = fma2(unpack_bf16x2(o[i].z), unpack_bf16x2(g.z), two);
+            two = fma2(unpack_bf16x2(o[i].w), unpack_bf16x2(g.w), two);
+            float d = two.x + two.y;
+#pragma unroll
+            for (int k = 1; k < kL; k *= 2) d += __shfl_xor_sync(0xffffffffu, d, k);
+            if (i == lane % kL) sum = d;
+          }
+        }
       }
+      // the four warps of a row add up
+      const int r = (warp & 3) * 32 + lane;
+      if (quarter > 0) share[(quarter - 1) * T + r] = sum;
+      ok = bar_sync_and<512>(1, ok);
+      if (!ok) break;
+      if (quarter == 0) {
+        const float delta = (sum + share[r]) + (share[T + r] + share[2 * T + r]);
+        share[r] = -delta;
+        if (mine) {
+          p.stat[static_cast<size_t>(h) * p.M + row] = nlse;
+          p.stat[static_cast<size_t>(p.heads + h) * p.M + row] = -delta;
+        }
+      }
+      ok = bar_sync_and<512>(1, ok);
+      const float ndelta = share[r];
       for (int j = 0; j < n && ok; ++j, ++step) {
         const int j0 = t.begin + j * T + 32 * quarter;                     // the first of this thread's 32 keys
         const uint32_t rS = tS + (step & 1u) * T + lanes + 32 * quarter;

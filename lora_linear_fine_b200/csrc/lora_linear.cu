@@ -2355,9 +2355,6 @@ lora_status_t launch_attn_bwd(const AttnParams& p, int sms, cudaStream_t st) {
   LORA_TRY(kernel_ready<q>(AttnDqCfg<D>::kSmemBytes));
   const int64_t ctas = static_cast<int64_t>(p.plan.max_q) * p.heads;
   if (ctas > (int64_t(1) << 31) - 1) return LORA_ERR_UNSUPPORTED;
-  launch_k(attn_delta_kernel<D>, dim3(static_cast<unsigned>(ceil_div(p.M, 32)), static_cast<unsigned>(ceil_div(p.heads, 8))),
-           dim3(256), 0, st, false, p);
-  LORA_TRY(check_launch("attn_delta_kernel"));
   launch_k(q, dim3(static_cast<unsigned>(std::min<int64_t>(ctas, sms))), dim3(kAttnBwdThreads), AttnDqCfg<D>::kSmemBytes,
            st, false, p, maps);
   LORA_TRY(check_launch("attn_dq_kernel"));
@@ -2445,7 +2442,7 @@ lora_status_t lora_linear_rotary_tables(const lora_rotary_table_desc* desc, floa
   RotaryTurns turns = {};
   rotary_turns(desc, &turns);
   const int pairs = desc->rot / 2;
-  const int64_t rows = 256 / (pairs / 4);
+  const int64_t rows = 256 / (pairs / 4) * kRotaryRun;
   const int64_t blocks = ceil_div(desc->n_pos, rows), cap = static_cast<int64_t>(dev.sms) * 8;
   launch_k(rotary_tables_kernel, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)), dim3(256), 0,
            static_cast<cudaStream_t>(stream), false, turns, pairs, static_cast<long long>(desc->n_pos),
