@@ -2443,7 +2443,7 @@ lora_status_t lora_linear_rotary_tables(const lora_rotary_table_desc* desc, floa
   rotary_turns(desc, &turns);
   const int pairs = desc->rot / 2;
   const int64_t rows = 256 / (pairs / 4) * kRotaryRun;
-  const int64_t blocks = ceil_div(desc->n_pos, rows), cap = static_cast<int64_t>(dev.sms) * 8;
+  const int64_t blocks = ceil_div(desc->n_pos, rows), cap = static_cast<int64_t>(dev.sms) * kRotaryTableCtas;
   launch_k(rotary_tables_kernel, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)), dim3(256), 0,
            static_cast<cudaStream_t>(stream), false, turns, pairs, static_cast<long long>(desc->n_pos),
            static_cast<float>(desc->amplitude), cos, sin);

@@ -29,11 +29,12 @@ struct RotaryTurns {
 // and walks over groups of four positions, 16 bytes of each table a step: the
 // first position's angle that way, the next three by turning it on by w, 2 w
 // and 3 w (two products and a sum each, within 3 * 2^-24 of the amplitude).
-// All four the first way took 60 instructions a value, half as long again as
-// the stores: 16 us for 131072 x 64 pairs.
+// 131072 x 64 pairs: 12.4 us (all four the first way, some 60 instructions a
+// value: 16.0 us; the stores alone 10.4 us).
 constexpr int kRotaryRun = 4;
+constexpr int kRotaryTableCtas = 2;     // an SM: more repeat the three turns more often than they help the stores
 
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, kRotaryTableCtas)
     rotary_tables_kernel(const __grid_constant__ RotaryTurns turns, int pairs, long long n_pos, float amplitude,
                          float* __restrict__ cos_t, float* __restrict__ sin_t) {
   const int quads = pairs / 4;
