@@ -20,6 +20,9 @@
 
 namespace lora {
 
+// Registers: 96 a thread at launch (the most for 640 threads), then 64 for the
+// first four warps and 104 for the others.
+constexpr int kAttnBwdRegsLow = 64, kAttnBwdRegsHigh = 104;
 constexpr int kAttnBwdThreads = 640;     // warps: TMA, MMA, statistics, trimming, 16 of elementwise work
 
 struct AttnBwdMaps {
@@ -154,198 +157,202 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     return s;
   };
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- TMA
-    if (lane == 0) {
-      RingPos rq;
-      uint32_t turn = 0;
+  if (warp < 4) {
+    regs_lower<kAttnBwdRegsLow>();
+    if (warp == 0) {
+      // ---------------------------------------------------------------- TMA
+      if (lane == 0) {
+        RingPos rq;
+        uint32_t turn = 0;
+        while (ok && items.advance()) {
+          if (items.behind()) continue;
+          const AttnTileRef t = items.t;
+          const Steps st = steps();
+          const int hk = st.hk, first = st.first;
+          int h = st.h, row = st.row;
+          for (int i = 0; i < st.n && ok; ++i) {
+            const bool trim = row + T > t.end;
+            for (int k = 0; k < 2 && ok; ++k) {
+              ok = mbar_wait(k == 0 ? &q_empty[rq.stage] : &o_empty[rq.stage], rq.phase ^ 1u, ctl);
+              if (!ok) break;
+              uint64_t* bar = k == 0 ? (trim ? &q_land[rq.stage] : &q_full[rq.stage])
+                                     : (trim ? &o_land[rq.stage] : &o_full[rq.stage]);
+              uint8_t* dst = (k == 0 ? ring_q : ring_o) + rq.stage * C::kTileBytes;
+              mbar_arrive_expect_tx(bar, C::kTileBytes);
+              for (int b = 0; b < C::kBoxes; ++b)
+                tma_load_2d(dst + b * (T * 128), k == 0 ? &maps.q : &maps.d_o, bar, h * D + 64 * b, row);
+            }
+            if (!ok) break;
+            rq.next(S);
+            if (i == 0) {
+              const uint32_t buf = turn % NB;
+              ok = mbar_wait(&kv_empty[buf], ((turn / NB) & 1u) ^ 1u, ctl);
+              if (!ok) break;
+              ++turn;
+              mbar_arrive_expect_tx(&kv_full[buf], 2 * C::kTileBytes);
+              for (int b = 0; b < C::kBoxes; ++b) {
+                tma_load_2d(sk + buf * C::kTileBytes + b * (T * 128), &maps.k, &kv_full[buf], hk * D + 64 * b, t.row0);
+                tma_load_2d(sv + buf * C::kTileBytes + b * (T * 128), &maps.v, &kv_full[buf], hk * D + 64 * b, t.row0);
+              }
+            }
+            row += T;
+            if (row >= t.end) { row = first; ++h; }
+          }
+        }
+        if (!ok) {   // every copy has landed before the CTA may end
+          for (uint32_t k = turn > NB ? turn - NB : 0; k < turn; ++k) mbar_wait(&kv_full[k % NB], (k / NB) & 1u, quiet);
+          attn_drain(q_full, S, rq);
+          attn_drain(o_full, S, rq);
+        }
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA
+      if (elect_one()) {
+        constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
+        constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
+        // a resident tile (keys) times a ring tile's rows
+        auto across = [&](const uint8_t* res, uint32_t buf, const uint8_t* ring, uint32_t stage, uint32_t d, uint64_t* bar) {
+          const uint64_t a = sdesc_sw128(smem_u32(res), 16, 1024) + buf * (C::kTileBytes >> 4);
+          const uint64_t b = sdesc_sw128(smem_u32(ring), 16, 1024) + stage * (C::kTileBytes >> 4);
+          {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
+              mma_bf16(d, a + off, b + off, kIdS, kk > 0);
+            }
+            mma_commit(bar);
+          }
+        };
+        // tensor memory (keys x queries) times a ring tile, which is free afterwards
+        auto along = [&](uint32_t a, uint64_t* ready, uint32_t parity, const uint8_t* ring, uint32_t stage, uint32_t d,
+                         bool fresh, uint64_t* bar) {
+          const uint64_t b = sdesc_sw128(smem_u32(ring), T * 128, 1024) + stage * (C::kTileBytes >> 4);
+#pragma unroll
+          for (int c = 0; c < kParts; ++c) {
+            if (!mbar_wait(&ready[c], parity, ctl)) return false;
+            tc_fence_after();
+            {
+#pragma unroll
+              for (int k = 0; k < T / 16 / kParts; ++k) {
+                const int kk = kParts == 2 ? attn_part_step<32>(c, k) : k;
+                mma_bf16_ta(d, a + attn_step_column<32>(kk), b + kk * (2048 >> 4), kIdO, !fresh || c + k > 0);
+              }
+              if (c == kParts - 1) mma_commit(bar);
+            }
+          }
+          return true;
+        };
+        RingPos r;
+        uint32_t turn = 0, step = 0;
+        while (ok && items.advance()) {
+          if (items.behind()) continue;
+          const int n = steps().n;
+          if (n == 0) continue;
+          const uint32_t buf = turn % NB;
+          ok = mbar_wait(&kv_full[buf], (turn / NB) & 1u, ctl) && mbar_wait(&q_full[r.stage], r.phase, ctl);
+          if (!ok) break;
+          tc_fence_after();
+          across(sk, buf, ring_q, r.stage, tS + step % NS * T, &s_full[step % NS]);
+          ok = mbar_wait(&o_full[r.stage], r.phase, ctl);
+          if (!ok) break;
+          tc_fence_after();
+          across(sv, buf, ring_o, r.stage, tP, dp_full);
+          if (n == 1) mma_commit(&kv_empty[buf]);
+          for (int i = 0; i < n && ok; ++i, ++step) {
+            RingPos nx = r;
+            nx.next(S);
+            const uint32_t tA = tS + step % NS * T, next = (step + 1) % NS;
+            auto next_scores = [&] {
+              if (!mbar_wait(&q_full[nx.stage], nx.phase, ctl)) return false;
+              tc_fence_after();
+              across(sk, buf, ring_q, nx.stage, tS + next * T, &s_full[next]);
+              return true;
+            };
+            if (NS == 2 && i + 1 < n) ok = next_scores();
+            // the accumulators of the item before have been read
+            if (i == 0) ok = ok && mbar_wait(acc_empty, (turn & 1u) ^ 1u, ctl);
+            ok = ok && along(tA, p_full, step & 1u, ring_o, r.stage, tV, i == 0, &o_empty[r.stage]);
+            if (NS == 1 && i + 1 < n) ok = ok && next_scores();
+            ok = ok && along(tP, ds_full, step & 1u, ring_q, r.stage, tK, i == 0, &q_empty[r.stage]);
+            if (!ok) break;
+            if (i + 1 < n) {
+              ok = mbar_wait(&o_full[nx.stage], nx.phase, ctl);
+              if (!ok) break;
+              tc_fence_after();
+              across(sv, buf, ring_o, nx.stage, tP, dp_full);
+              if (i + 2 == n) mma_commit(&kv_empty[buf]);
+            }
+            r = nx;
+          }
+          if (ok) mma_commit(acc_full);
+          ++turn;
+        }
+        mma_commit(mma_done);
+        mbar_wait(mma_done, 0, quiet);
+      }
+    } else if (warp == 2) {
+      // ---------------------------------------------------------------- row statistics
+      // Rows past the document: lse = infinity makes their p zero.
+      RingPos r;
       while (ok && items.advance()) {
         if (items.behind()) continue;
         const AttnTileRef t = items.t;
         const Steps st = steps();
-        const int hk = st.hk, first = st.first;
+        const int first = st.first;
         int h = st.h, row = st.row;
         for (int i = 0; i < st.n && ok; ++i) {
-          const bool trim = row + T > t.end;
-          for (int k = 0; k < 2 && ok; ++k) {
-            ok = mbar_wait(k == 0 ? &q_empty[rq.stage] : &o_empty[rq.stage], rq.phase ^ 1u, ctl);
-            if (!ok) break;
-            uint64_t* bar = k == 0 ? (trim ? &q_land[rq.stage] : &q_full[rq.stage])
-                                   : (trim ? &o_land[rq.stage] : &o_full[rq.stage]);
-            uint8_t* dst = (k == 0 ? ring_q : ring_o) + rq.stage * C::kTileBytes;
-            mbar_arrive_expect_tx(bar, C::kTileBytes);
-            for (int b = 0; b < C::kBoxes; ++b)
-              tma_load_2d(dst + b * (T * 128), k == 0 ? &maps.q : &maps.d_o, bar, h * D + 64 * b, row);
+          const float* a = p.stat + static_cast<size_t>(h) * p.M;
+          const float* b = a + static_cast<size_t>(p.heads) * p.M;
+          float l[4], d[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int m = row + e * 32 + lane;
+            l[e] = m < t.end ? a[m] : -INFINITY;
+            d[e] = m < t.end ? b[m] : 0.0f;
           }
+          ok = mbar_wait_warp(&st_empty[r.stage], r.phase ^ 1u, ctl);
           if (!ok) break;
-          rq.next(S);
-          if (i == 0) {
-            const uint32_t buf = turn % NB;
-            ok = mbar_wait(&kv_empty[buf], ((turn / NB) & 1u) ^ 1u, ctl);
-            if (!ok) break;
-            ++turn;
-            mbar_arrive_expect_tx(&kv_full[buf], 2 * C::kTileBytes);
-            for (int b = 0; b < C::kBoxes; ++b) {
-              tma_load_2d(sk + buf * C::kTileBytes + b * (T * 128), &maps.k, &kv_full[buf], hk * D + 64 * b, t.row0);
-              tma_load_2d(sv + buf * C::kTileBytes + b * (T * 128), &maps.v, &kv_full[buf], hk * D + 64 * b, t.row0);
-            }
+          float* s = stat + r.stage * 2 * T;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[e * 32 + lane] = l[e];
+            s[T + e * 32 + lane] = d[e];
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&st_full[r.stage]);
+          r.next(S);
           row += T;
           if (row >= t.end) { row = first; ++h; }
         }
       }
-      if (!ok) {   // every copy has landed before the CTA may end
-        for (uint32_t k = turn > NB ? turn - NB : 0; k < turn; ++k) mbar_wait(&kv_full[k % NB], (k / NB) & 1u, quiet);
-        attn_drain(q_full, S, rq);
-        attn_drain(o_full, S, rq);
-      }
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA
-    if (elect_one()) {
-      constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
-      constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
-      // a resident tile (keys) times a ring tile's rows
-      auto across = [&](const uint8_t* res, uint32_t buf, const uint8_t* ring, uint32_t stage, uint32_t d, uint64_t* bar) {
-        const uint64_t a = sdesc_sw128(smem_u32(res), 16, 1024) + buf * (C::kTileBytes >> 4);
-        const uint64_t b = sdesc_sw128(smem_u32(ring), 16, 1024) + stage * (C::kTileBytes >> 4);
-        {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
-            mma_bf16(d, a + off, b + off, kIdS, kk > 0);
-          }
-          mma_commit(bar);
-        }
-      };
-      // tensor memory (keys x queries) times a ring tile, which is free afterwards
-      auto along = [&](uint32_t a, uint64_t* ready, uint32_t parity, const uint8_t* ring, uint32_t stage, uint32_t d,
-                       bool fresh, uint64_t* bar) {
-        const uint64_t b = sdesc_sw128(smem_u32(ring), T * 128, 1024) + stage * (C::kTileBytes >> 4);
-#pragma unroll
-        for (int c = 0; c < kParts; ++c) {
-          if (!mbar_wait(&ready[c], parity, ctl)) return false;
-          tc_fence_after();
-          {
-#pragma unroll
-            for (int k = 0; k < T / 16 / kParts; ++k) {
-              const int kk = kParts == 2 ? attn_part_step<32>(c, k) : k;
-              mma_bf16_ta(d, a + attn_step_column<32>(kk), b + kk * (2048 >> 4), kIdO, !fresh || c + k > 0);
-            }
-            if (c == kParts - 1) mma_commit(bar);
-          }
-        }
-        return true;
-      };
-      RingPos r;
-      uint32_t turn = 0, step = 0;
+    } else if (warp == 3) {
+      // ---------------------------------------------------------------- trimming
+      // Rows past the document in its last query tile become zero: their p and
+      // ds are zero, but zero times an infinity or NaN there would not be.
+      uint32_t slot = 0, landed = 0;     // ring slots so far; a bit a stage: parity of its next landing
       while (ok && items.advance()) {
         if (items.behind()) continue;
-        const int n = steps().n;
-        if (n == 0) continue;
-        const uint32_t buf = turn % NB;
-        ok = mbar_wait(&kv_full[buf], (turn / NB) & 1u, ctl) && mbar_wait(&q_full[r.stage], r.phase, ctl);
-        if (!ok) break;
-        tc_fence_after();
-        across(sk, buf, ring_q, r.stage, tS + step % NS * T, &s_full[step % NS]);
-        ok = mbar_wait(&o_full[r.stage], r.phase, ctl);
-        if (!ok) break;
-        tc_fence_after();
-        across(sv, buf, ring_o, r.stage, tP, dp_full);
-        if (n == 1) mma_commit(&kv_empty[buf]);
-        for (int i = 0; i < n && ok; ++i, ++step) {
-          RingPos nx = r;
-          nx.next(S);
-          const uint32_t tA = tS + step % NS * T, next = (step + 1) % NS;
-          auto next_scores = [&] {
-            if (!mbar_wait(&q_full[nx.stage], nx.phase, ctl)) return false;
-            tc_fence_after();
-            across(sk, buf, ring_q, nx.stage, tS + next * T, &s_full[next]);
-            return true;
-          };
-          if (NS == 2 && i + 1 < n) ok = next_scores();
-          // the accumulators of the item before have been read
-          if (i == 0) ok = ok && mbar_wait(acc_empty, (turn & 1u) ^ 1u, ctl);
-          ok = ok && along(tA, p_full, step & 1u, ring_o, r.stage, tV, i == 0, &o_empty[r.stage]);
-          if (NS == 1 && i + 1 < n) ok = ok && next_scores();
-          ok = ok && along(tP, ds_full, step & 1u, ring_q, r.stage, tK, i == 0, &q_empty[r.stage]);
-          if (!ok) break;
-          if (i + 1 < n) {
-            ok = mbar_wait(&o_full[nx.stage], nx.phase, ctl);
+        const AttnTileRef t = items.t;
+        const Steps st = steps();
+        const int keep = (t.end - st.first) % T;
+        // steps of the document's last query tile
+        int i = (t.end - st.row + T - 1) / T - 1;
+        for (; i < st.n && ok && keep != 0; i += st.n_tiles) {
+          const uint32_t stage = (slot + i) % S;
+          for (int k = 0; k < 2 && ok; ++k) {
+            ok = mbar_wait_warp(k == 0 ? &q_land[stage] : &o_land[stage], (landed >> stage) & 1u, ctl);
             if (!ok) break;
-            tc_fence_after();
-            across(sv, buf, ring_o, nx.stage, tP, dp_full);
-            if (i + 2 == n) mma_commit(&kv_empty[buf]);
+            attn_trim_tile<C::kBoxes>((k == 0 ? ring_q : ring_o) + stage * C::kTileBytes, keep, lane);
+            if (lane == 0) mbar_arrive(k == 0 ? &q_full[stage] : &o_full[stage]);
           }
-          r = nx;
+          landed ^= 1u << stage;
         }
-        if (ok) mma_commit(acc_full);
-        ++turn;
+        slot += st.n;
       }
-      mma_commit(mma_done);
-      mbar_wait(mma_done, 0, quiet);
-    }
-  } else if (warp == 2) {
-    // ---------------------------------------------------------------- row statistics
-    // Rows past the document: lse = infinity makes their p zero.
-    RingPos r;
-    while (ok && items.advance()) {
-      if (items.behind()) continue;
-      const AttnTileRef t = items.t;
-      const Steps st = steps();
-      const int first = st.first;
-      int h = st.h, row = st.row;
-      for (int i = 0; i < st.n && ok; ++i) {
-        const float* a = p.stat + static_cast<size_t>(h) * p.M;
-        const float* b = a + static_cast<size_t>(p.heads) * p.M;
-        float l[4], d[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int m = row + e * 32 + lane;
-          l[e] = m < t.end ? a[m] : -INFINITY;
-          d[e] = m < t.end ? b[m] : 0.0f;
-        }
-        ok = mbar_wait_warp(&st_empty[r.stage], r.phase ^ 1u, ctl);
-        if (!ok) break;
-        float* s = stat + r.stage * 2 * T;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[e * 32 + lane] = l[e];
-          s[T + e * 32 + lane] = d[e];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&st_full[r.stage]);
-        r.next(S);
-        row += T;
-        if (row >= t.end) { row = first; ++h; }
-      }
-    }
-  } else if (warp == 3) {
-    // ---------------------------------------------------------------- trimming
-    // Rows past the document in its last query tile become zero: their p and
-    // ds are zero, but zero times an infinity or NaN there would not be.
-    uint32_t slot = 0, landed = 0;     // ring slots so far; a bit a stage: parity of its next landing
-    while (ok && items.advance()) {
-      if (items.behind()) continue;
-      const AttnTileRef t = items.t;
-      const Steps st = steps();
-      const int keep = (t.end - st.first) % T;
-      // steps of the document's last query tile
-      int i = (t.end - st.row + T - 1) / T - 1;
-      for (; i < st.n && ok && keep != 0; i += st.n_tiles) {
-        const uint32_t stage = (slot + i) % S;
-        for (int k = 0; k < 2 && ok; ++k) {
-          ok = mbar_wait_warp(k == 0 ? &q_land[stage] : &o_land[stage], (landed >> stage) & 1u, ctl);
-          if (!ok) break;
-          attn_trim_tile<C::kBoxes>((k == 0 ? ring_q : ring_o) + stage * C::kTileBytes, keep, lane);
-          if (lane == 0) mbar_arrive(k == 0 ? &q_full[stage] : &o_full[stage]);
-        }
-        landed ^= 1u << stage;
-      }
-      slot += st.n;
     }
   } else {
     // ---------------------------------------------------------------- elementwise
+    regs_raise<kAttnBwdRegsHigh>();
     const int quarter = (warp - 4) >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t rP = tP + lanes + 32 * quarter;
@@ -604,142 +611,146 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
   const int group = p.heads / p.kv_heads;
   bool ok = true;
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- TMA
-    if (lane == 0) {
-      RingPos rk, rv;
-      uint32_t turn = 0;
-      while (ok && items.advance()) {
-        if (items.behind()) continue;
-        const AttnTileRef t = items.t;
-        const int h = items.h, hk = h / group, n = attn_key_tiles(t, t.row0, T);
-        for (int j = 0; j < n && ok; ++j) {
-          const int row = t.begin + j * T;
-          const bool trim = row + T > t.end;     // rows past the document become zero, as in attn_dkv_kernel
-          for (int k = 0; k < 2 && ok; ++k) {
-            RingPos& r = k == 0 ? rk : rv;
-            ok = mbar_wait(k == 0 ? &k_empty[r.stage] : &v_empty[r.stage], r.phase ^ 1u, ctl);
-            if (!ok) break;
-            uint8_t* dst = (k == 0 ? ring_k : ring_v) + r.stage * C::kTileBytes;
-            uint64_t* bar = k == 0 ? (trim ? &k_land[r.stage] : &k_full[r.stage])
-                                   : (trim ? &v_land[r.stage] : &v_full[r.stage]);
-            mbar_arrive_expect_tx(bar, C::kTileBytes);
-            for (int b = 0; b < C::kBoxes; ++b)
-              tma_load_2d(dst + b * (T * 128), k == 0 ? &maps.k : &maps.v, bar, hk * D + 64 * b, row);
-            r.next(k == 0 ? SK : SV);
-            if (j == 0 && k == 0) {
-              ok = mbar_wait(qo_empty, (turn & 1u) ^ 1u, ctl);
+  if (warp < 4) {
+    regs_lower<kAttnBwdRegsLow>();
+    if (warp == 0) {
+      // ---------------------------------------------------------------- TMA
+      if (lane == 0) {
+        RingPos rk, rv;
+        uint32_t turn = 0;
+        while (ok && items.advance()) {
+          if (items.behind()) continue;
+          const AttnTileRef t = items.t;
+          const int h = items.h, hk = h / group, n = attn_key_tiles(t, t.row0, T);
+          for (int j = 0; j < n && ok; ++j) {
+            const int row = t.begin + j * T;
+            const bool trim = row + T > t.end;     // rows past the document become zero, as in attn_dkv_kernel
+            for (int k = 0; k < 2 && ok; ++k) {
+              RingPos& r = k == 0 ? rk : rv;
+              ok = mbar_wait(k == 0 ? &k_empty[r.stage] : &v_empty[r.stage], r.phase ^ 1u, ctl);
               if (!ok) break;
-              ++turn;
-              mbar_arrive_expect_tx(qo_full, 2 * C::kTileBytes);
-              for (int b = 0; b < C::kBoxes; ++b) {
-                tma_load_2d(sq + b * (T * 128), &maps.q, qo_full, h * D + 64 * b, t.row0);
-                tma_load_2d(so + b * (T * 128), &maps.d_o, qo_full, h * D + 64 * b, t.row0);
+              uint8_t* dst = (k == 0 ? ring_k : ring_v) + r.stage * C::kTileBytes;
+              uint64_t* bar = k == 0 ? (trim ? &k_land[r.stage] : &k_full[r.stage])
+                                     : (trim ? &v_land[r.stage] : &v_full[r.stage]);
+              mbar_arrive_expect_tx(bar, C::kTileBytes);
+              for (int b = 0; b < C::kBoxes; ++b)
+                tma_load_2d(dst + b * (T * 128), k == 0 ? &maps.k : &maps.v, bar, hk * D + 64 * b, row);
+              r.next(k == 0 ? SK : SV);
+              if (j == 0 && k == 0) {
+                ok = mbar_wait(qo_empty, (turn & 1u) ^ 1u, ctl);
+                if (!ok) break;
+                ++turn;
+                mbar_arrive_expect_tx(qo_full, 2 * C::kTileBytes);
+                for (int b = 0; b < C::kBoxes; ++b) {
+                  tma_load_2d(sq + b * (T * 128), &maps.q, qo_full, h * D + 64 * b, t.row0);
+                  tma_load_2d(so + b * (T * 128), &maps.d_o, qo_full, h * D + 64 * b, t.row0);
+                }
               }
             }
           }
         }
-      }
-      if (!ok) {   // every copy has landed before the CTA may end
-        mbar_wait(qo_full, (turn & 1u) ^ 1u, quiet);
-        attn_drain(k_full, SK, rk);
-        attn_drain(v_full, SV, rv);
-      }
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA
-    if (elect_one()) {
-      constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
-      constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
-      auto across = [&](const uint8_t* res, const uint8_t* ring, uint32_t stage, uint32_t d, uint64_t* bar, uint64_t* bar2) {
-        const uint64_t a = sdesc_sw128(smem_u32(res), 16, 1024);
-        const uint64_t b = sdesc_sw128(smem_u32(ring), 16, 1024) + stage * (C::kTileBytes >> 4);
-        {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
-            mma_bf16(d, a + off, b + off, kIdS, kk > 0);
-          }
-          mma_commit(bar);
-          if (bar2 != nullptr) mma_commit(bar2);
+        if (!ok) {   // every copy has landed before the CTA may end
+          mbar_wait(qo_full, (turn & 1u) ^ 1u, quiet);
+          attn_drain(k_full, SK, rk);
+          attn_drain(v_full, SV, rv);
         }
-      };
-      RingPos ks, kd, v;             // K tiles of the scores, of dQ; V tiles
-      uint32_t turn = 0, issued = 0, step = 0;      // items; score tiles issued; dS tiles taken
-      auto scores = [&]() {
-        if (!mbar_wait(&k_full[ks.stage], ks.phase, ctl)) return false;
-        tc_fence_after();
-        across(sq, ring_k, ks.stage, tS + (issued & 1u) * T, &s_full[issued & 1u], nullptr);
-        ++issued;
-        ks.next(SK);
-        return true;
-      };
-      auto values = [&]() {
-        if (!mbar_wait(&v_full[v.stage], v.phase, ctl)) return false;
-        tc_fence_after();
-        across(so, ring_v, v.stage, tP, dp_full, &v_empty[v.stage]);
-        v.next(SV);
-        return true;
-      };
-      while (ok && items.advance()) {
-        if (items.behind()) continue;
-        const int n = attn_key_tiles(items.t, items.t.row0, T);
-        ok = mbar_wait(qo_full, turn & 1u, ctl);
-        ok = ok && scores() && values();
-        if (n > 1) ok = ok && scores();
-        if (ok && n == 1) mma_commit(qo_empty);
-        // the accumulator of the item before has been read
-        ok = ok && mbar_wait(acc_empty, (turn & 1u) ^ 1u, ctl);
-        for (int j = 0; j < n && ok; ++j, ++step) {
-          ok = mbar_wait(ds_full, step & 1u, ctl);
-          if (!ok) break;
-          tc_fence_after();
-          if (j + 1 < n) {
-            ok = values();
-            if (!ok) break;
-            if (j + 2 == n) mma_commit(qo_empty);       // the last use of Q and dO
-          }
-          const uint64_t b = sdesc_sw128(smem_u32(ring_k), T * 128, 1024) + kd.stage * (C::kTileBytes >> 4);
-          const uint32_t a = tS + (step & 1u) * T;
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA
+      if (elect_one()) {
+        constexpr uint32_t kIdS = idesc_bf16(T, T, false, false);
+        constexpr uint32_t kIdO = idesc_bf16(T, D, false, true);
+        auto across = [&](const uint8_t* res, const uint8_t* ring, uint32_t stage, uint32_t d, uint64_t* bar, uint64_t* bar2) {
+          const uint64_t a = sdesc_sw128(smem_u32(res), 16, 1024);
+          const uint64_t b = sdesc_sw128(smem_u32(ring), 16, 1024) + stage * (C::kTileBytes >> 4);
           {
 #pragma unroll
-            for (int kk = 0; kk < T / 16; ++kk)
-              mma_bf16_ta(tQ, a + attn_step_column<32>(kk), b + kk * (2048 >> 4), kIdO, j > 0 || kk > 0);
-            mma_commit(&k_empty[kd.stage]);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk / 4) * (T * 128) + (kk % 4) * 32) >> 4;
+              mma_bf16(d, a + off, b + off, kIdS, kk > 0);
+            }
+            mma_commit(bar);
+            if (bar2 != nullptr) mma_commit(bar2);
           }
-          kd.next(SK);
-          if (j + 2 < n) ok = scores();
+        };
+        RingPos ks, kd, v;             // K tiles of the scores, of dQ; V tiles
+        uint32_t turn = 0, issued = 0, step = 0;      // items; score tiles issued; dS tiles taken
+        auto scores = [&]() {
+          if (!mbar_wait(&k_full[ks.stage], ks.phase, ctl)) return false;
+          tc_fence_after();
+          across(sq, ring_k, ks.stage, tS + (issued & 1u) * T, &s_full[issued & 1u], nullptr);
+          ++issued;
+          ks.next(SK);
+          return true;
+        };
+        auto values = [&]() {
+          if (!mbar_wait(&v_full[v.stage], v.phase, ctl)) return false;
+          tc_fence_after();
+          across(so, ring_v, v.stage, tP, dp_full, &v_empty[v.stage]);
+          v.next(SV);
+          return true;
+        };
+        while (ok && items.advance()) {
+          if (items.behind()) continue;
+          const int n = attn_key_tiles(items.t, items.t.row0, T);
+          ok = mbar_wait(qo_full, turn & 1u, ctl);
+          ok = ok && scores() && values();
+          if (n > 1) ok = ok && scores();
+          if (ok && n == 1) mma_commit(qo_empty);
+          // the accumulator of the item before has been read
+          ok = ok && mbar_wait(acc_empty, (turn & 1u) ^ 1u, ctl);
+          for (int j = 0; j < n && ok; ++j, ++step) {
+            ok = mbar_wait(ds_full, step & 1u, ctl);
+            if (!ok) break;
+            tc_fence_after();
+            if (j + 1 < n) {
+              ok = values();
+              if (!ok) break;
+              if (j + 2 == n) mma_commit(qo_empty);       // the last use of Q and dO
+            }
+            const uint64_t b = sdesc_sw128(smem_u32(ring_k), T * 128, 1024) + kd.stage * (C::kTileBytes >> 4);
+            const uint32_t a = tS + (step & 1u) * T;
+            {
+#pragma unroll
+              for (int kk = 0; kk < T / 16; ++kk)
+                mma_bf16_ta(tQ, a + attn_step_column<32>(kk), b + kk * (2048 >> 4), kIdO, j > 0 || kk > 0);
+              mma_commit(&k_empty[kd.stage]);
+            }
+            kd.next(SK);
+            if (j + 2 < n) ok = scores();
+          }
+          if (ok) mma_commit(acc_full);
+          ++turn;
         }
-        if (ok) mma_commit(acc_full);
-        ++turn;
+        mma_commit(mma_done);
+        mbar_wait(mma_done, 0, quiet);
       }
-      mma_commit(mma_done);
-      mbar_wait(mma_done, 0, quiet);
-    }
-  } else if (warp == 2) {
-    // ---------------------------------------------------------------- trimming
-    uint32_t slot = 0, k_landed = 0, v_landed = 0;
-    while (ok && items.advance()) {
-      if (items.behind()) continue;
-      const AttnTileRef t = items.t;
-      const int n = attn_key_tiles(t, t.row0, T), row = t.begin + (n - 1) * T;
-      slot += n;
-      if (row + T > t.end) {
-        const uint32_t sk = (slot - 1) % SK, sv = (slot - 1) % SV;
-        ok = mbar_wait_warp(&k_land[sk], (k_landed >> sk) & 1u, ctl);
-        if (!ok) break;
-        attn_trim_tile<C::kBoxes>(ring_k + sk * C::kTileBytes, t.end - row, lane);
-        if (lane == 0) mbar_arrive(&k_full[sk]);
-        ok = mbar_wait_warp(&v_land[sv], (v_landed >> sv) & 1u, ctl);
-        if (!ok) break;
-        attn_trim_tile<C::kBoxes>(ring_v + sv * C::kTileBytes, t.end - row, lane);
-        if (lane == 0) mbar_arrive(&v_full[sv]);
-        k_landed ^= 1u << sk;
-        v_landed ^= 1u << sv;
+    } else if (warp == 2) {
+      // ---------------------------------------------------------------- trimming
+      uint32_t slot = 0, k_landed = 0, v_landed = 0;
+      while (ok && items.advance()) {
+        if (items.behind()) continue;
+        const AttnTileRef t = items.t;
+        const int n = attn_key_tiles(t, t.row0, T), row = t.begin + (n - 1) * T;
+        slot += n;
+        if (row + T > t.end) {
+          const uint32_t sk = (slot - 1) % SK, sv = (slot - 1) % SV;
+          ok = mbar_wait_warp(&k_land[sk], (k_landed >> sk) & 1u, ctl);
+          if (!ok) break;
+          attn_trim_tile<C::kBoxes>(ring_k + sk * C::kTileBytes, t.end - row, lane);
+          if (lane == 0) mbar_arrive(&k_full[sk]);
+          ok = mbar_wait_warp(&v_land[sv], (v_landed >> sv) & 1u, ctl);
+          if (!ok) break;
+          attn_trim_tile<C::kBoxes>(ring_v + sv * C::kTileBytes, t.end - row, lane);
+          if (lane == 0) mbar_arrive(&v_full[sv]);
+          k_landed ^= 1u << sk;
+          v_landed ^= 1u << sv;
+        }
       }
     }
-  } else if (warp >= 4) {
+  } else {
     // ---------------------------------------------------------------- elementwise
+    regs_raise<kAttnBwdRegsHigh>();
     const int quarter = (warp - 4) >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t rP = tP + lanes + 32 * quarter;

@@ -2351,8 +2351,9 @@ lora_status_t launch_attn_bwd(const AttnParams& p, int sms, cudaStream_t st) {
     return LORA_ERR_CUDA;
   constexpr auto kv = attn_dkv_kernel<D, kCap, kBias>;
   constexpr auto q = attn_dq_kernel<D, kCap, kBias>;
-  LORA_TRY(kernel_ready<kv>(AttnDkvCfg<D>::kSmemBytes));
-  LORA_TRY(kernel_ready<q>(AttnDqCfg<D>::kSmemBytes));
+  constexpr int kRegs = 128 * (kAttnBwdRegsLow + 4 * kAttnBwdRegsHigh);
+  LORA_TRY(kernel_ready<kv>(AttnDkvCfg<D>::kSmemBytes, kAttnBwdThreads, kRegs));
+  LORA_TRY(kernel_ready<q>(AttnDqCfg<D>::kSmemBytes, kAttnBwdThreads, kRegs));
   const int64_t ctas = static_cast<int64_t>(p.plan.max_q) * p.heads;
   if (ctas > (int64_t(1) << 31) - 1) return LORA_ERR_UNSUPPORTED;
   launch_k(q, dim3(static_cast<unsigned>(std::min<int64_t>(ctas, sms))), dim3(kAttnBwdThreads), AttnDqCfg<D>::kSmemBytes,
