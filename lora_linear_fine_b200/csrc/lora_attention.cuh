@@ -241,12 +241,13 @@ __device__ __forceinline__ float2 pair_of(const uint32_t* v) {
 // 2^x of a pair on the FMA pipe: x = n + f with n whole and |f| <= 1/2 (adding
 // 1.5 * 2^23 leaves n in the low bits), 2^f by a polynomial of degree 5 that is
 // 1 at 0 with the least largest relative error on that interval (2^-22.5 in
-// fp32), n added to the exponent.  Below -126 the result is 2^-126.  The special function unit gives
-// 16 exponentials a cycle and SM, fewer than a tile's products leave time for;
-// so the kernels form part of them this way.
+// fp32), n added to the exponent.  From -127 down the result is 0 (1 with 127
+// taken off its exponent).  The special function unit gives 16 exponentials a
+// cycle and SM, fewer than a tile's products leave time for; so the kernels
+// form part of them this way.
 __device__ __forceinline__ float2 exp2_poly(float2 x) {
   constexpr float kRound = 12582912.0f;
-  x = make_float2(max_nan(x.x, -126.0f), max_nan(x.y, -126.0f));
+  x = make_float2(max_nan(x.x, -127.0f), max_nan(x.y, -127.0f));
   const float2 t = add2(x, both(kRound));
   const float2 f = fma2(add2(t, both(-kRound)), both(-1.0f), x);
   float2 p = fma2(both(0.001326472731307149f), f, both(0.009671512991189957f));

@@ -20,9 +20,10 @@
 // row's first tile and moves only when a later score lies more than 2^16 above
 // it.  Until then P and the row's sum l are larger by the same factor, which
 // fp32 and bf16 hold as well, and the rescaling of O in tensor memory (a read
-// and a write of all of it) is rare.  Scores under a cap up to 66 need no
-// maximum: exponents of 2 within +-96 are taken as they are (m = 0).  P is
-// rounded to bf16 for the tensor core; l adds the fp32 values.
+// and a write of all of it) is rare.  Scores under a cap up to 55 need no
+// maximum: exponents of 2 within +-80 are taken as they are (m = 0; V may lie
+// within 2^+-26 over rows of 2^20 keys even where all scores are at the cap).
+// P is rounded to bf16 for the tensor core; l adds the fp32 values.
 //
 // The softmax goes through its 128 columns in pieces of 32, in loops that are
 // not unrolled: all of it in registers and in line is 40 KB of code with a cap
@@ -43,6 +44,8 @@ struct AttnFwdCfg {
   static_assert(kSmemBytes <= kSmemLimitBytes, "shared memory");
 };
 constexpr int kAttnFwdThreads = 384;     // warps: TMA, MMA, trimming, one idle, softmax of tile a (4), of tile b (4)
+
+constexpr float kAttnFixedRange = 80.0f;
 
 struct AttnFwdMaps {
   CUtensorMap q, k, v;     // [M x heads * D] bf16, box 64 x 128, 128-byte swizzle
@@ -286,7 +289,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
       const int see = min(max(row + 1, t.prefix_end), t.end);              // keys [begin, see)
       const int all = min(max(t.row0 + x * T + 1, t.prefix_end), t.end);   // ... that every row sees
       score.head(p, h);
-      const bool fixed = kCap && score.mul <= 96.0f && score.slope2 >= 0.0f;
+      const bool fixed = kCap && score.mul <= kAttnFixedRange && score.slope2 >= 0.0f;
       float m = fixed ? 0.0f : -INFINITY;      // the reference, an exponent of 2
       float2 l = make_float2(0.0f, 0.0f);      // two partial sums
       for (int j = nx - 1; j >= 0 && ok; --j, ++step) {

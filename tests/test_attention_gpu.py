@@ -143,6 +143,36 @@ def test_scale_and_large_scores():
     _check([260, 100], 0, 2, 1, 128, spread=1.6, seed=13)
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(slopes=[0.01, -0.005]), dict(cap=100.0), dict(cap=100.0, slopes=[0.02, -0.01])],
+                         ids=["plain", "bias", "cap", "both"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_far_keys_dominate(D, kw):
+    """Scores that rise by tens from the nearest tile to the far ones: the
+    running reference moves, for some rows and not for others."""
+    def edit(Q, K, V, dO):
+        K[:100] *= 6.0
+        K[200:260] *= 3.0
+
+    lens = [600, 90]
+    out, x, _, _ = _run(lens, 0, 2, 1, D, seed=21, edit=edit, cap=kw.get("cap", 0.0), slopes=kw.get("slopes"))
+    Q, K, V, dO = (G.host_f64(t) for t in x)
+    slopes = None if kw.get("slopes") is None else np.array(kw["slopes"], dtype=np.float32).astype(float)
+    ref = O.attention(Q, K, V, _starts(lens), 2, 1, softcap=kw.get("cap", 0.0), slopes=slopes, dO=dO)
+    # scores up to 2^6: their fp32 error 2^-24 2^6 2^2 turns into a relative
+    # 2^-16 of p; the roundings of p, ds and the outputs (2^-9 rms) remain
+    for name in ("O", "dQ", "dK", "dV"):
+        off = np.linalg.norm(G.host_f64(out[name]) - ref[name]) / np.linalg.norm(ref[name])
+        assert off <= 2.0 ** -7, f"{name}: {off:.3g}"
+    assert np.abs(G.host_f64(out["lse"]) - ref["lse"]).max() <= 2.0 ** -14
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("cap", [0.0, 10.0, 70.0])
+def test_rising_bias(cap, causal):
+    """Negative slopes favour the far keys."""
+    _check([200, 77, 260], 0, 4, 2, 64, slopes=[-0.5, 0.0, -2.0 ** -8, 0.25], cap=cap, causal=causal, seed=22)
+
+
 def test_rows_behind_the_last_document():
     """Zeros and -inf, whatever the inputs hold there; no document changes."""
     import torch
