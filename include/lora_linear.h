@@ -541,9 +541,9 @@ lora_status_t lora_linear_ce_fwd_bwd(const lora_ce_desc* desc, const void* H, co
  *   Y = bf16((x - mean) * rstd * g + b).
  * X [M x d] bf16, g [d] bf16, b [d] bf16 or NULL (no shift); Y [M x d] bf16,
  * mean [M] and rstd [M] fp32 (written; the backward's inputs).  Sums in fp32.
- * Y may be X.  8 <= d <= 16384 (LORA_ERR_UNSUPPORTED above), d % 8 == 0 and X, g, b, Y 16-byte, mean
- * and rstd 4-byte aligned (LORA_ERR_ALIGNMENT); eps >= 0 and finite, M >= 0
- * (LORA_ERR_INVALID_ARG).  M == 0 launches nothing. */
+ * Y may be X.  8 <= d <= 16384 (LORA_ERR_UNSUPPORTED above), d % 8 == 0 and
+ * X, g, b, Y 16-byte, mean and rstd 4-byte aligned (LORA_ERR_ALIGNMENT); eps >= 0
+ * and finite, M >= 0 (LORA_ERR_INVALID_ARG).  M == 0 launches nothing. */
 lora_status_t lora_linear_layernorm_fwd(const void* X, const void* g, const void* b, int64_t M, int64_t d, float eps,
                                         void* Y, float* mean, float* rstd, void* stream);
 
@@ -556,8 +556,9 @@ size_t lora_linear_layernorm_workspace_size(int64_t M, int64_t d);
  *   dg = sum over tokens of dY * x_hat, db = sum over tokens of dY.
  * dY [M x d]: bf16 (dy_f32 == 0; e.g. a projection's dX), or fp32 (dy_f32 == 1;
  * the sum that lora_linear_bwd_rope leaves).  dX [M x d] bf16; dg, db [d] fp32
- * (written, 4-byte aligned; each may be NULL).  dX may be dY when dY is bf16, or X.  dg and db are summed in
- * fp32 in an order fixed by M, d and the device: the same bits in every call.
+ * (written, 4-byte aligned; each may be NULL).  dX may be dY when dY is bf16, or
+ * X.  dg and db are summed in fp32 in an order fixed by M, d and the device: the
+ * same bits in every call.  Status bit 0x1 of the workspace: a wait gave up.
  * M == 0 zero-fills dg and db.  Other checks as the forward;
  * workspace >= lora_linear_layernorm_workspace_size(M, d) bytes. */
 lora_status_t lora_linear_layernorm_bwd(const void* dY, int dy_f32, const void* X, const void* g, const float* mean,
@@ -659,9 +660,11 @@ lora_status_t lora_linear_attn_plan(const int32_t* starts, const int32_t* prefix
  * bf16, lse [M x heads] fp32 (written; natural logarithm); slopes: device fp32
  * [heads] or NULL.  plan: of this M, n_docs and causal; a plan of other sizes
  * sets its status bit 0x2 and nothing is computed.  A document whose rows hold
- * infinities or NaN leaves the other documents' results as they are.  No
- * workspace.  p is rounded to bf16 for the product with v; scores, sums and
- * outputs are accumulated in fp32. */
+ * infinities or NaN leaves the other documents' results as they are; within the
+ * document they may reach any row (a product with a p of zero).  A wait inside
+ * the kernels that gives up sets the plan's status bit 0x1.  No workspace.  p
+ * is rounded to bf16 for the product with v; scores, sums and outputs are
+ * accumulated in fp32. */
 lora_status_t lora_linear_attn_fwd(const lora_attn_desc* desc, void* plan, size_t plan_bytes, const void* Q,
                                    const void* K, const void* V, const float* slopes, void* O, float* lse,
                                    void* stream);
@@ -671,9 +674,10 @@ size_t lora_linear_attn_workspace_size(const lora_attn_desc* desc);
 
 /* Backward: dQ, dK, dV (bf16, the shapes of Q, K, V) from dO (bf16) and the
  * forward's O and lse.  The gradients of shared key / value heads are summed
- * over their query heads in fp32 in a fixed order (no atomics): the same bits
- * in every call.  slopes get no gradient (frozen).  p and ds are rounded to
- * bf16 for their products.
+ * over their query heads in fp32 in an order fixed by M, n_docs and the heads
+ * (no atomics): the same bits in every call.  slopes get no gradient (frozen).
+ * p and ds are rounded to bf16 for their products; sum_j p_ij dp_ij is formed in
+ * fp32 for rows that see up to 128 keys, from the bf16 O otherwise.
  * workspace >= lora_linear_attn_workspace_size(desc) bytes. */
 lora_status_t lora_linear_attn_bwd(const lora_attn_desc* desc, void* plan, size_t plan_bytes, const void* dO,
                                    const void* Q, const void* K, const void* V, const void* O, const float* lse,

@@ -22,6 +22,20 @@ rotated) is a sequence of calls on one stream:
 
 with rope = make_rope_desc(pos, cos, sin, n_pos, head_dim) and dXn an fp32
 [M x d] buffer that the q call writes and the k and v calls add to.
+
+The rest of an attention block, as torch functions over a batch of packed
+documents (``layer_norm`` in place of the RMSNorm, ``rotary`` for layouts that
+the projections' epilogue does not cover, ``attention``):
+
+    plan = AttentionPlan(starts, M)                 # once a batch, for all layers
+    cos, sin = rotary_tables(n_pos, rot)            # once a model
+    Xn, mean, rstd = layer_norm(X, g, b)
+    q, k, v = (forward(Xn, W, A, B, s)[0] for W, A, B in ...)
+    q, k = rotary(q, k, pos, cos, sin, head_dim)
+    O, lse = attention(q, k, v, plan, heads, kv_heads)
+    dq, dk, dv = attention_backward(dO, q, k, v, O, lse, plan, heads, kv_heads)
+    dq, dk = rotary(dq, dk, pos, cos, sin, head_dim, inverse=True)
+    dX, dg, db = layer_norm_backward(dXn, X, g, mean, rstd)
 """
 from __future__ import annotations
 
