@@ -221,10 +221,38 @@ class _LazyLib:
     def __getattr__(self, name):
         if _LazyLib._h is None:
             _LazyLib._h = _load()
-        return getattr(_LazyLib._h, name)
+        f = getattr(_LazyLib._h, name)
+        setattr(self, name, f)
+        return f
 
 
 _lib = _LazyLib()
+
+
+class _LazyTorch:
+    """The torch functions' short way into the library (csrc/lora_torch.cpp), loaded on first use like it."""
+
+    def __getattr__(self, name):
+        import importlib.util
+        path = os.path.join(_PKG, "_lora_torch.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it with `python -m lora_linear_fine_b200.build`")
+        import torch  # noqa: F401  (the module is linked with torch's libraries)
+        spec = importlib.util.spec_from_file_location("_lora_torch", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        self.__dict__.update({k: v for k, v in vars(module).items() if not k.startswith("__")})
+        return self.__dict__[name]
+
+
+_torch = _LazyTorch()
+
+
+def _done(result, what):
+    """The outputs of a call through _torch; a number is its status."""
+    if type(result) is int:
+        raise LoraError(result, what)
+    return result
 
 
 # ---------------------------------------------------------------------------
@@ -723,6 +751,8 @@ def layer_norm(X, g, b=None, eps=1e-5, stream=None):
     scale g and shift b (bf16 [d]; b may be None); mean, rstd fp32 [M] are the
     backward's inputs."""
     import torch
+    if stream is None and (out := _torch.layer_norm(X, g, b, eps)) is not None:
+        return _done(out, "lora_linear_layernorm_fwd")
     if X.dim() != 2:
         _refuse(f"X has shape {tuple(X.shape)}")
     M, d = X.shape
@@ -743,6 +773,9 @@ def layer_norm_backward(dY, X, g, mean, rstd, bias=True, workspace=None, stream=
     """(dX, dg, db) for dY bf16 or fp32 [M x d]; dg, db fp32 [d] (db None
     without ``bias``)."""
     import torch
+    if stream is None and workspace is not None and (
+            out := _torch.layer_norm_backward(dY, X, g, mean, rstd, bias, workspace.buf)) is not None:
+        return _done(out, "lora_linear_layernorm_bwd")
     if X.dim() != 2:
         _refuse(f"X has shape {tuple(X.shape)}")
     M, d = X.shape
@@ -774,6 +807,9 @@ def rotary_tables(n_pos, rot, base=10000.0, scaling="none", factor=1.0, low=1.0,
         _refuse(f"scaling {scaling!r} is none of {sorted(ROTARY_SCALINGS)}")
     if n_pos < 0 or rot < 0:
         _refuse(f"n_pos {n_pos}, rot {rot}")
+    if device is None and stream is None and torch.cuda.is_initialized():
+        return _done(_torch.rotary_tables(n_pos, rot, base, ROTARY_SCALINGS[scaling], factor, low, high, original,
+                                          amplitude), "lora_linear_rotary_tables")
     if device is None:
         device = torch.device("cuda", torch.cuda.current_device()) if stream is None else stream.device
     device = torch.device(device)
@@ -795,6 +831,9 @@ def rotary(Q, K, pos, cos, sin, head_dim, layout="half", inverse=False, inplace=
     [n_pos x rot/2]; the first rot features of each head take part.
     ``inverse`` turns back: the gradients of Q and K from those of Yq and Yk."""
     import torch
+    if stream is None and workspace is not None and not inplace and layout in ROTARY_LAYOUTS and (
+            out := _torch.rotary(Q, K, pos, cos, sin, head_dim, ROTARY_LAYOUTS[layout], inverse, workspace.buf)) is not None:
+        return _done(out, "lora_linear_rotary")
     if layout not in ROTARY_LAYOUTS:
         _refuse(f"layout {layout!r} is none of {sorted(ROTARY_LAYOUTS)}")
     if Q.dim() != 2 or cos.dim() != 2:
@@ -872,6 +911,9 @@ def attention(Q, K, V, plan, heads, kv_heads, scale=None, softcap=0.0, slopes=No
     [heads]) subtract slope * |i - j|.  lse fp32 [M x heads] is the backward's
     input."""
     import torch
+    if stream is None and (out := _torch.attention(Q, K, V, plan.buf, plan.M, plan.n_docs, plan.causal, heads, kv_heads,
+                                                   scale, softcap, slopes)) is not None:
+        return _done(out, "lora_linear_attn_fwd")
     desc = _attention_args(Q, K, V, plan, heads, kv_heads, scale, softcap, slopes)
     device = Q.device
 
@@ -889,6 +931,10 @@ def attention_backward(dO, Q, K, V, O, lse, plan, heads, kv_heads, scale=None, s
                        workspace=None, stream=None):
     """(dQ, dK, dV) of ``attention`` for its O and lse."""
     import torch
+    if stream is None and workspace is not None and (
+            out := _torch.attention_backward(dO, Q, K, V, O, lse, plan.buf, plan.M, plan.n_docs, plan.causal, heads,
+                                             kv_heads, scale, softcap, slopes, workspace.buf)) is not None:
+        return _done(out, "lora_linear_attn_bwd")
     desc = _attention_args(Q, K, V, plan, heads, kv_heads, scale, softcap, slopes)
     device = Q.device
     _tensors(device, ("dO", dO, torch.bfloat16, Q.shape), ("O", O, torch.bfloat16, Q.shape),
