@@ -152,7 +152,7 @@ struct AttnParams {
   float* lse;                    // [M x heads]
   float* stat;                   // backward: [2][heads][M], lse log2(e) and delta
   float* partial;                // backward: [parts][2][M x kv_heads * D] sums of dk and dv (parts > 1)
-  int parts;
+  int parts, parts_log2;
   int M, n_docs, heads, kv_heads;
   float scale, cap;              // cap 0: none
 };
@@ -173,13 +173,14 @@ struct AttnItems {
   AttnTileRef t;
   int h;
   __device__ __forceinline__ AttnItems(const AttnTileRef* list, uint32_t tiles, int heads)
-      : t{0, 0, 0, 0}, h(0), list_(list), heads_(static_cast<uint32_t>(heads)), total_(tiles * heads_) {
+      : t{0, 0, 0, 0}, h(0), list_(list), heads_(static_cast<uint32_t>(heads)), total_(tiles * heads_),
+        inverse_(0xffffffffu / heads_) {
     fetch();
   }
   __device__ __forceinline__ bool advance() {
-    if (at_ >= total_) return false;
+    if (!more_) return false;
     t = next_;
-    h = static_cast<int>(at_ % heads_);
+    h = next_h_;
     ++round_;
     fetch();
     return true;
@@ -188,11 +189,19 @@ struct AttnItems {
 
  private:
   __device__ __forceinline__ void fetch() {
-    at_ = round_ * gridDim.x + ((round_ & 1u) ? gridDim.x - 1u - blockIdx.x : blockIdx.x);
-    if (at_ < total_) next_ = list_[at_ / heads_];
+    const uint32_t at = round_ * gridDim.x + ((round_ & 1u) ? gridDim.x - 1u - blockIdx.x : blockIdx.x);
+    more_ = at < total_;
+    if (!more_) return;
+    // at / heads: the product with the inverse is the quotient or one less (at < 2^31)
+    uint32_t q = __umulhi(at, inverse_), r = at - q * heads_;
+    if (r >= heads_) { ++q; r -= heads_; }
+    next_h_ = static_cast<int>(r);
+    next_ = list_[q];
   }
   const AttnTileRef* list_;
-  uint32_t heads_, total_, round_ = 0, at_ = 0;
+  uint32_t heads_, total_, inverse_, round_ = 0;
+  bool more_ = false;
+  int next_h_ = 0;
   AttnTileRef next_{0, 0, 0, 0};
 };
 

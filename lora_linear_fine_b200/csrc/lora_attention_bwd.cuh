@@ -144,16 +144,20 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
   struct Steps { int hk, part, first, n_tiles, n, h, row; };
   auto steps = [&] {
     Steps s;
-    s.hk = items.h / p.parts;
-    s.part = items.h - s.hk * p.parts;
     s.first = items.t.row0 < items.t.prefix_end ? items.t.begin : items.t.row0;
     s.n_tiles = (items.t.end - s.first + T - 1) / T;
-    const long long all = static_cast<long long>(s.n_tiles) * group;
-    const int from = static_cast<int>(all * s.part / p.parts);
-    s.n = static_cast<int>(all * (s.part + 1) / p.parts) - from;
-    const int g = from / s.n_tiles;
-    s.h = s.hk * group + g;
-    s.row = s.first + (from - g * s.n_tiles) * T;
+    s.hk = items.h >> p.parts_log2;
+    s.part = items.h & (p.parts - 1);
+    s.n = s.n_tiles * group;
+    s.h = s.hk * group;
+    s.row = s.first;
+    if (p.parts > 1) {       // few rows then: within 32 bits
+      const int from = s.n * s.part >> p.parts_log2;
+      s.n = (s.n * (s.part + 1) >> p.parts_log2) - from;
+      const int g = from / s.n_tiles;
+      s.h += g;
+      s.row += (from - g * s.n_tiles) * T;
+    }
     return s;
   };
 
@@ -368,7 +372,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       const AttnTileRef t = items.t;
       if (items.behind()) {
         const int last = min(t.row0 + T, t.end), i = threadIdx.x - 128;
-        const int hk = items.h / p.parts, part = items.h - hk * p.parts;
+        const int hk = items.h >> p.parts_log2, part = items.h & (p.parts - 1);
         if (p.parts == 1) {
           attn_zero_rows<D>(p.dK, p.kv_heads, hk, t.row0, last, i, 512);
           attn_zero_rows<D>(p.dV, p.kv_heads, hk, t.row0, last, i, 512);

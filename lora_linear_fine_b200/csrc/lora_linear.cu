@@ -2567,6 +2567,7 @@ lora_status_t lora_linear_attn_bwd(const lora_attn_desc* d, void* plan, size_t p
   p.stat = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes + attn_stat_bytes(d));
   p.parts = attn_bwd_parts(d);
+  while ((1 << p.parts_log2) < p.parts) ++p.parts_log2;
   return d->head_dim == 64 ? launch_attn_bwd_mod<64>(p, dev.sms, static_cast<cudaStream_t>(stream))
                            : launch_attn_bwd_mod<128>(p, dev.sms, static_cast<cudaStream_t>(stream));
 }
