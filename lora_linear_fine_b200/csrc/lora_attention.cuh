@@ -153,6 +153,7 @@ struct AttnParams {
   float* stat;                   // backward: [2][heads][M], lse log2(e) and delta
   float* partial;                // backward: [parts][2][M x kv_heads * D] sums of dk and dv (parts > 1)
   int parts, parts_log2;
+  int single;                    // forward: items of one tile
   int M, n_docs, heads, kv_heads;
   float scale, cap;              // cap 0: none
 };

@@ -99,7 +99,12 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
   uint64_t* kv_full = st_empty + S;    // [NB]
   uint64_t* kv_empty = kv_full + NB;   // [NB]
   uint64_t* s_full = kv_empty + NB;    // [NS]
-  uint64_t* p_full = s_full + NS;      // [2] parts of P from all warps
+  // [NS][kParts] parts of P from all warps.  One a buffer of S: with two, a
+  // warp may be at the next tile's P before another has finished this one's.
+  // [NS][kParts]: a part of P from all warps.  One a buffer of S: with two of
+  // them a warp may be at the next tile's P before another has finished this one's.
+  uint64_t* p_full = s_full + NS;
+  static_assert(NS * kParts == 2, "the barriers of P");
   uint64_t* dp_full = p_full + 2;
   uint64_t* ds_full = dp_full + 1;     // [2]
   uint64_t* acc_full = ds_full + 2;    // dk and dv of the item are complete
@@ -275,7 +280,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             if (NS == 2 && i + 1 < n) ok = next_scores();
             // the accumulators of the item before have been read
             if (i == 0) ok = ok && mbar_wait(acc_empty, (turn & 1u) ^ 1u, ctl);
-            ok = ok && along(tA, p_full, step & 1u, ring_o, r.stage, tV, i == 0, &o_empty[r.stage]);
+            ok = ok && along(tA, p_full + step % NS * kParts, step / NS & 1u, ring_o, r.stage, tV, i == 0, &o_empty[r.stage]);
             if (NS == 1 && i + 1 < n) ok = ok && next_scores();
             ok = ok && along(tP, ds_full, step & 1u, ring_q, r.stage, tK, i == 0, &q_empty[r.stage]);
             if (!ok) break;
@@ -428,7 +433,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
               g[k / 2] = kCap ? mul2(y, g[k / 2]) : y;
             }
             attn_put_part<kParts>(rS, e0 / (32 / kParts), w);
-            attn_publish(&p_full[e0 / (32 / kParts)], lane);
+            attn_publish(&p_full[step % NS * kParts + e0 / (32 / kParts)], lane);
           }
         }
         // the first row of a document without a longer prefix sees one key

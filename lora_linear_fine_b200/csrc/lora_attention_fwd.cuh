@@ -100,12 +100,15 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
   // so none of its CTAs can take what a CTA of this grid still waits for.
   grid_dep_wait();
 
-  AttnItems items(p.plan.fwd, attn_plan_ok(p) ? p.plan.head[kPlanFwd] : 0u, p.heads);
+  // Items of one tile where pairs would leave SMs idle.
+  AttnItems items(p.single ? p.plan.q : p.plan.fwd, attn_plan_ok(p) ? p.plan.head[p.single ? kPlanQ : kPlanFwd] : 0u,
+                  p.heads);
+  auto pair = [&] { return !p.single && items.t.row0 + T < items.t.end; };
   bool ok = true;
   // key tiles that the rows of the item's two tiles see
   auto tiles_of = [&](int* n_a) {
     *n_a = attn_key_tiles(items.t, items.t.row0, T);
-    return items.t.row0 + T < items.t.end ? attn_key_tiles(items.t, items.t.row0 + T, T) : *n_a;
+    return pair() ? attn_key_tiles(items.t, items.t.row0 + T, T) : *n_a;
   };
 
   if (warp < 4) {
@@ -118,7 +121,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
           if (items.behind()) continue;
           const AttnTileRef t = items.t;
           const int h = items.h, hk = h / (p.heads / p.kv_heads);
-          const int tiles_x = t.row0 + T < t.end ? 2 : 1;
+          const int tiles_x = pair() ? 2 : 1;
           int n_a;
           const int n = tiles_of(&n_a);
           for (int i = 0; i < 2 * n && ok; ++i) {
@@ -185,7 +188,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
         uint32_t q_turn = 0, o_turn[2] = {0, 0}, step[2] = {0, 0};      // of Q; of O; key tiles of a and b
         while (ok && items.advance()) {
           if (items.behind()) continue;
-          const int tiles_x = items.t.row0 + T < items.t.end ? 2 : 1;
+          const int tiles_x = pair() ? 2 : 1;
           int n_a;
           const int n = tiles_of(&n_a);
           // tile a begins with its own first key tile, which may be b's second
@@ -276,7 +279,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
       const AttnTileRef t = items.t;
       const int h = items.h;
       if (items.behind()) {
-        const int last = min(t.row0 + 2 * T, t.end);
+        const int last = min(t.row0 + (p.single ? T : 2 * T), t.end);
         attn_zero_rows<D>(p.O, p.heads, h, t.row0, last, threadIdx.x - 128, 256);
         const int r = t.row0 + static_cast<int>(threadIdx.x) - 128;
         if (r < last) p.lse[static_cast<size_t>(r) * p.heads + h] = -INFINITY;
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
       const int row = t.row0 + x * T + (warp & 3) * 32 + lane;
       int n_a;
       const int n = tiles_of(&n_a);
-      const int nx = x == 0 ? n_a : (t.row0 + T < t.end ? n : 0);
+      const int nx = x == 0 ? n_a : (pair() ? n : 0);
       const int see = min(max(row + 1, t.prefix_end), t.end);              // keys [begin, see)
       const int all = min(max(t.row0 + x * T + 1, t.prefix_end), t.end);   // ... that every row sees
       score.head(p, h);

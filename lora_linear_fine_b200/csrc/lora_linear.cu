@@ -2302,13 +2302,13 @@ AttnParams attn_params(const lora_attn_desc* d, void* plan, const void* Q, const
 }
 
 // Shares that the steps of a dk / dv item are cut into: as many as bring the
-// items to twice the SMs, but no more than 8 (nor than the query heads and
-// tiles of a document give steps for).
+// items to twice the SMs, up to 8, with four steps at least in a share of a
+// document of mean length (a step takes 1.5 us, adding the shares up 5 us).
 int attn_bwd_parts(const lora_attn_desc* d) {
   const int64_t tiles = ceil_div(d->M, kAttnTile), items = (tiles + d->n_docs) * d->kv_heads;
   const int64_t steps = (d->heads / d->kv_heads) * ceil_div(d->M, kAttnTile * std::max<int64_t>(1, d->n_docs));
   int parts = 1;
-  while (parts < 8 && items * parts < 2 * kTargetCtas && parts < steps) parts *= 2;
+  while (parts < 8 && items * parts < 2 * kTargetCtas && 8 * parts <= steps) parts *= 2;
   return parts;
 }
 
@@ -2330,7 +2330,7 @@ lora_status_t launch_attn_fwd(const AttnParams& p, int sms, cudaStream_t st) {
     return LORA_ERR_CUDA;
   constexpr auto k = attn_fwd_kernel<D, kCap, kBias>;
   LORA_TRY(kernel_ready<k>(AttnFwdCfg<D>::kSmemBytes));
-  const int64_t ctas = static_cast<int64_t>(p.plan.max_fwd) * p.heads;
+  const int64_t ctas = static_cast<int64_t>(p.single ? p.plan.max_q : p.plan.max_fwd) * p.heads;
   if (ctas > (int64_t(1) << 31) - 1) return LORA_ERR_UNSUPPORTED;
   launch_k(k, dim3(static_cast<unsigned>(std::min<int64_t>(ctas, sms))), dim3(kAttnFwdThreads), AttnFwdCfg<D>::kSmemBytes, st, false, p, maps);
   return check_launch("attn_fwd_kernel");
@@ -2529,6 +2529,8 @@ lora_status_t lora_linear_attn_fwd(const lora_attn_desc* d, void* plan, size_t p
   LORA_TRY(check_arch(&dev));
   if (d->M == 0) return LORA_OK;
   AttnParams p = attn_params(d, plan, Q, K, V, slopes, lse);
+  // A pair of tiles takes 1.4 times one: single ones while pairs do not fill the SMs.
+  p.single = (ceil_div(d->M, 2 * kAttnTile) + d->n_docs) * d->heads < dev.sms;
   p.O = static_cast<__nv_bfloat16*>(O);
   return d->head_dim == 64 ? launch_attn_fwd_mod<64>(p, dev.sms, static_cast<cudaStream_t>(stream))
                            : launch_attn_fwd_mod<128>(p, dev.sms, static_cast<cudaStream_t>(stream));
