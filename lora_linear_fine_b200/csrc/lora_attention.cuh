@@ -306,51 +306,46 @@ struct AttnScore {
   __device__ __forceinline__ void head(const AttnParams& p, int h) {
     if constexpr (kBias) slope2 = p.slopes[h] * kLog2e;
   }
-  // 32 kChunks products of a row become values; dt: 1 - tanh^2 (only with a cap).
-  template <int kChunks, bool kWantDt>
-  __device__ __forceinline__ void values(uint32_t (&v)[kChunks][32], float2* dt) const {
+  // n products of a row become values; dt: 1 - tanh^2 (only with a cap).
+  template <bool kWantDt, int n>
+  __device__ __forceinline__ void values(uint32_t (&v)[n], float2* dt) const {
     if constexpr (kCap) {
       float top[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          top[0] = max3_abs(top[0], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
-          top[1] = max3_abs(top[1], __uint_as_float(v[c][e + 2]), __uint_as_float(v[c][e + 3]));
-        }
+      for (int e = 0; e < n; e += 4) {
+        top[0] = max3_abs(top[0], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+        top[1] = max3_abs(top[1], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+      }
       if (!__any_sync(0xffffffffu, fmaxf(top[0], top[1]) > limit)) {
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 s = pair_of(&v[c][e]), u = mul2(s, s);
-            float2 q = fma2(both(a3), u, both(a2));
-            q = fma2(q, u, both(a1));
-            q = fma2(q, u, both(a0));
-            put(v[c], e, mul2(s, q));
-          }
+        for (int e = 0; e < n; e += 2) {
+          const float2 s = pair_of(&v[e]), u = mul2(s, s);
+          float2 q = fma2(both(a3), u, both(a2));
+          q = fma2(q, u, both(a1));
+          q = fma2(q, u, both(a0));
+          put(v, e, mul2(s, q));
+        }
       } else {
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            v[c][e] = __float_as_uint(
-                fmaf(-2.0f, rcp_approx(1.0f + ex2(__uint_as_float(v[c][e]) * (2.0f * kLog2e * pre))), 1.0f));
+        for (int e = 0; e < n; ++e) v[e] = __float_as_uint(far(__uint_as_float(v[e])));
       }
       if constexpr (kWantDt) {
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 t = pair_of(&v[c][e]);
-            dt[16 * c + e / 2] = fma2(mul2(t, t), both(-1.0f), both(1.0f));
-          }
+        for (int e = 0; e < n; e += 2) {
+          const float2 t = pair_of(&v[e]);
+          dt[e / 2] = fma2(mul2(t, t), both(-1.0f), both(1.0f));
+        }
       }
     }
   }
   // one product's value
   __device__ __forceinline__ float one(float s) const {
-    return kCap ? fmaf(-2.0f, rcp_approx(1.0f + ex2(s * (2.0f * kLog2e * pre))), 1.0f) : s;
+    if constexpr (!kCap) return s;
+    const float u = s * s;
+    return fabsf(s) <= limit ? s * fmaf(fmaf(fmaf(a3, u, a2), u, a1), u, a0) : far(s);
+  }
+  __device__ __forceinline__ float far(float s) const {
+    return fmaf(-2.0f, rcp_approx(1.0f + ex2(s * (2.0f * kLog2e * pre))), 1.0f);
   }
   // `base` minus the bias at distances d0 + c and d0 + c + 1 (either sign)
   __device__ __forceinline__ float2 shifted(float2 base, float d0, float c, float step) const {
@@ -358,7 +353,8 @@ struct AttnScore {
     const float2 d = add2(both(d0), make_float2(c, c + step));
     return make_float2(fmaf(-slope2, fabsf(d.x), base.x), fmaf(-slope2, fabsf(d.y), base.y));
   }
-  __device__ __forceinline__ static void put(uint32_t (&v)[32], int e, float2 z) {
+  template <int n>
+  __device__ __forceinline__ static void put(uint32_t (&v)[n], int e, float2 z) {
     v[e] = __float_as_uint(z.x);
     v[e + 1] = __float_as_uint(z.y);
   }

@@ -13,7 +13,10 @@
 // is as much as dp - delta itself for rows that see a few keys.  So for rows
 // whose keys all lie in one tile it is sum_j p_ij dp_ij in fp32, and a row that
 // sees one key has ds = 0 exactly.  attn_dq_kernel leaves delta and lse by head
-// for attn_dkv_kernel.
+// for attn_dkv_kernel.  With a bias few keys count in long documents too: the
+// sum is then formed on the way for dk, and dq takes ds in two bf16 parts
+// (8192 tokens in 23 documents, cap and bias: dk off by 2.4e-3 of its norm
+// instead of 2.7e-3, dq by 2.2e-3 instead of 2.7e-3; 87 us instead of 72).
 #pragma once
 
 #include "lora_attention.cuh"
@@ -404,7 +407,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         float2 g[16];                     // p, then p d(cap tanh)
         tmem_ld32(rS, v[0]);
         tmem_wait_ld();
-        score.template values<1, true>(v, g);
+        score.template values<true>(v[0], g);
         const float d0 = static_cast<float>(i0 - key);
         const bool part = !all_keys && tile0 < t.row0 + T;
         const int lim = key < t.prefix_end ? 0 : key - i0;             // queries from this one on see the key
@@ -712,17 +715,22 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
             ok = mbar_wait(ds_full, step & 1u, ctl);
             if (!ok) break;
             tc_fence_after();
+            const uint64_t b = sdesc_sw128(smem_u32(ring_k), T * 128, 1024) + kd.stage * (C::kTileBytes >> 4);
             if (j + 1 < n) {
               ok = values();
               if (!ok) break;
               if (j + 2 == n) mma_commit(qo_empty);       // the last use of Q and dO
             }
-            const uint64_t b = sdesc_sw128(smem_u32(ring_k), T * 128, 1024) + kd.stage * (C::kTileBytes >> 4);
             const uint32_t a = tS + (step & 1u) * T;
             {
 #pragma unroll
               for (int kk = 0; kk < T / 16; ++kk)
                 mma_bf16_ta(tQ, a + attn_step_column<32>(kk), b + kk * (2048 >> 4), kIdO, j > 0 || kk > 0);
+              if constexpr (kBias) {       // what bf16 leaves of dS
+#pragma unroll
+                for (int kk = 0; kk < T / 16; ++kk)
+                  mma_bf16_ta(tQ, a + 16 + attn_step_column<32>(kk), b + kk * (2048 >> 4), kIdO, 1);
+              }
               mma_commit(&k_empty[kd.stage]);
             }
             kd.next(SK);
@@ -782,23 +790,36 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       score.head(p, h);
       const float2 shift = both(nlse);
       const bool lone = see - t.begin == 1;
-      uint32_t v[1][32];
-      // p of 32 keys from the products in v
-      auto probabilities = [&](float2 (&y)[16], float2 (&dt)[16], int j0) {
-        score.template values<1, true>(v, dt);
+      // p of N keys from the products in v: all 32 of the thread at once, or, with
+      // a cap, whose derivative takes registers too, 16
+      constexpr int N = kCap || kBias ? 16 : 32;
+      auto probabilities = [&](uint32_t (&v)[N], float2 (&y)[N / 2], float2 (&dt)[N / 2], int j0) {
+        score.template values<true>(v, dt);
         const float d0 = static_cast<float>(j0 - row);
 #pragma unroll
-        for (int e = 0; e < 32; e += 2)
+        for (int e = 0; e < N; e += 2)
           y[e / 2] = attn_exp2<AttnScore<kCap, kBias>::kPoly>(
-              fma2(pair_of(&v[0][e]), mul, score.shifted(shift, d0, e, 1.0f)), e / 2);
-        if (j0 + 32 > all) {
+              fma2(pair_of(&v[e]), mul, score.shifted(shift, d0, e, 1.0f)), e / 2);
+        if (j0 + N > all) {
           const int lim = see - j0;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < N / 2; ++i) {
             if (2 * i >= lim) y[i].x = 0.0f;
             if (2 * i + 1 >= lim) y[i].y = 0.0f;
           }
         }
+      };
+      // The four warps of a row add up; the first one's sum counts.
+      const int r = (warp & 3) * 32 + lane;
+      auto whole_row = [&](float part, bool good) {
+        if (quarter > 0) share[(quarter - 1) * T + r] = part;
+        if (!bar_sync_and<512>(1, good)) return false;
+        if (quarter == 0) {
+          const float delta = (part + share[r]) + (share[T + r] + share[2 * T + r]);
+          share[r] = -delta;
+          if (mine) p.stat[static_cast<size_t>(p.heads + h) * p.M + row] = -delta;
+        }
+        return bar_sync_and<512>(1, true);
       };
       // delta: a quarter of the row's terms here
       float sum = 0.0f;
@@ -807,14 +828,19 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         ok = mbar_wait_warp(&s_full[step & 1u], (step >> 1) & 1u, ctl) && mbar_wait_warp(dp_full, step & 1u, ctl);
         if (ok) {
           tc_fence_after();
-          float2 y[16], dt[16], two = make_float2(0.0f, 0.0f);
-          tmem_ld32(tS + (step & 1u) * T + lanes + 32 * quarter, v[0]);
-          tmem_wait_ld();
-          probabilities(y, dt, t.begin + 32 * quarter);
-          tmem_ld32(rP, v[0]);
-          tmem_wait_ld();
+          float2 two = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+          for (int c = 0; c < 32; c += N) {
+            uint32_t v[N];
+            float2 y[N / 2], dt[N / 2];
+            tmem_ld(tS + (step & 1u) * T + lanes + 32 * quarter + c, v);
+            tmem_wait_ld();
+            probabilities(v, y, dt, t.begin + 32 * quarter + c);
+            tmem_ld(rP + c, v);
+            tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) two = fma2(y[e / 2], pair_of(&v[0][e]), two);
+            for (int e = 0; e < N; e += 2) two = fma2(y[e / 2], pair_of(&v[e]), two);
+          }
           sum = two.x + two.y;
         }
       } else {
@@ -845,50 +871,57 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
           }
         }
       }
-      // the four warps of a row add up
-      const int r = (warp & 3) * 32 + lane;
-      if (quarter > 0) share[(quarter - 1) * T + r] = sum;
-      ok = bar_sync_and<512>(1, ok);
+      if (quarter == 0 && mine) p.stat[static_cast<size_t>(h) * p.M + row] = nlse;
+      ok = whole_row(sum, ok);
       if (!ok) break;
-      if (quarter == 0) {
-        const float delta = (sum + share[r]) + (share[T + r] + share[2 * T + r]);
-        share[r] = -delta;
-        if (mine) {
-          p.stat[static_cast<size_t>(h) * p.M + row] = nlse;
-          p.stat[static_cast<size_t>(p.heads + h) * p.M + row] = -delta;
-        }
-      }
-      ok = bar_sync_and<512>(1, ok);
       const float ndelta = share[r];
+      float2 exact = make_float2(0.0f, 0.0f);      // sum_j p_ij dp_ij, for the dk / dv kernel
       for (int j = 0; j < n && ok; ++j, ++step) {
         const int j0 = t.begin + j * T + 32 * quarter;                     // the first of this thread's 32 keys
         const uint32_t rS = tS + (step & 1u) * T + lanes + 32 * quarter;
         ok = mbar_wait_warp(&s_full[step & 1u], (step >> 1) & 1u, ctl);
         if (!ok) break;
         tc_fence_after();
-        float2 g[16], dt[16];             // g: p d(cap tanh)
-        tmem_ld32(rS, v[0]);
-        tmem_wait_ld();
-        probabilities(g, dt, j0);
+        uint32_t low[32 / N][N / 2];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if constexpr (kCap) g[i] = mul2(g[i], dt[i]);
-          if (lone) g[i] = make_float2(0.0f, 0.0f);
+        for (int c = 0; c < 32 / N; ++c) {
+          uint32_t v[N], w[N / 2];
+          float2 y[N / 2], dt[N / 2];
+          tmem_ld(rS + N * c, v);
+          tmem_wait_ld();
+          probabilities(v, y, dt, j0 + N * c);
+#pragma unroll
+          for (int i = 0; i < N / 2; ++i)
+            if (lone) y[i] = make_float2(0.0f, 0.0f);
+          if (c == 0) {
+            ok = mbar_wait_warp(dp_full, step & 1u, ctl);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          tmem_ld(rP + N * c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < N; e += 2) {
+            const float2 dp = pair_of(&v[e]);
+            if constexpr (kBias) exact = fma2(y[e / 2], dp, exact);
+            float2 ds = mul2(y[e / 2], add2(dp, both(ndelta)));
+            if constexpr (kCap) ds = mul2(ds, dt[e / 2]);
+            w[e / 2] = pack_bf16x2(ds.x, ds.y);
+            if constexpr (kBias) {
+              const float2 rest = fma2(unpack_bf16x2(w[e / 2]), both(-1.0f), ds);
+              low[c][e / 2] = pack_bf16x2(rest.x, rest.y);
+            }
+          }
+          tmem_st(rS + N / 2 * c, w);           // over columns that this warp has read
         }
-        ok = mbar_wait_warp(dp_full, step & 1u, ctl);
+        if constexpr (kBias) {
+#pragma unroll
+          for (int c = 0; c < 32 / N; ++c) tmem_st(rS + 16 + N / 2 * c, low[c]);
+        }
         if (!ok) break;
-        tc_fence_after();
-        tmem_ld32(rP, v[0]);
-        tmem_wait_ld();
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float2 y = mul2(g[e / 2], add2(pair_of(&v[0][e]), both(ndelta)));
-          w[e / 2] = pack_bf16x2(y.x, y.y);
-        }
-        tmem_st16(rS, w);
         attn_publish(ds_full, lane);
       }
+      if (kBias && n > 1) ok = whole_row(exact.x + exact.y, ok);
       ok = ok && mbar_wait_warp(acc_full, turn & 1u, ctl);
       if (!ok) break;
       ++turn;

@@ -292,7 +292,9 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
       const int see = min(max(row + 1, t.prefix_end), t.end);              // keys [begin, see)
       const int all = min(max(t.row0 + x * T + 1, t.prefix_end), t.end);   // ... that every row sees
       score.head(p, h);
-      const bool fixed = kCap && score.mul <= kAttnFixedRange && score.slope2 >= 0.0f;
+      // rows of few keys take their maximum: p of the only key, or of one that
+      // outweighs the others, is then 1 and needs no rounding
+      const bool fixed = kCap && nx > 1 && score.mul <= kAttnFixedRange && score.slope2 >= 0.0f;
       float m = fixed ? 0.0f : -INFINITY;      // the reference, an exponent of 2
       float2 l = make_float2(0.0f, 0.0f);      // two partial sums
       for (int j = nx - 1; j >= 0 && ok; --j, ++step) {
@@ -323,7 +325,8 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
             tmem_wait_ld();
             if (part) hide(half);
             if (kBias && exact) {
-              score.template values<2, false>(v, nullptr);
+              score.template values<false>(v[0], nullptr);
+              score.template values<false>(v[1], nullptr);
 #pragma unroll
               for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -383,7 +386,8 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           tmem_wait_ld();
-          score.template values<2, false>(v, nullptr);
+          score.template values<false>(v[0], nullptr);
+          score.template values<false>(v[1], nullptr);
           if (part) hide(half);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {

@@ -150,6 +150,25 @@ def test_rows_that_see_one_key(D, cap, causal):
     assert (np.abs(got - want) <= (2.0 ** -7 * (1 + 2.0 ** -9) if cap else 0.0) * np.abs(want)).all()
 
 
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("cap", [2.0, 50.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_key_with_a_cap(D, cap, bias):
+    """One key a row and scores near zero: O is V, and lse is the score to the
+    precision of the score, not of a sum of exponentials near one."""
+    lens = [1] * 9
+    kw = dict(slopes=[0.25, 0.01]) if bias else {}
+    out, (Q, K, V, _), _, _ = _run(lens, 0, 2, 1, D, cap=cap, scale=0.002, seed=21, **kw)
+    # p is 1 but for 2^-16, which bf16 rounds away in p and again in the quotient
+    want = G.host_f64(V.view(9, 1, D).expand(9, 2, D))
+    assert np.array_equal(G.host_f64(out["O"].view(9, 2, D)), want)
+    terms = G.host_f64(Q).reshape(9, 2, D) * G.host_f64(K).reshape(9, 1, D) * 0.002
+    z = cap * np.tanh(terms.sum(-1) / cap)
+    # the sum of D products in fp32, and some ten roundings of the result
+    tol = 2.0 ** -24 * (D * np.abs(terms).sum(-1) + 16 * np.abs(z))
+    assert (np.abs(G.host_f64(out["lse"]).reshape(9, 2) - z) <= tol).all()
+
+
 def test_gradients_of_short_documents():
     """Rows with a few keys: delta is not the one of the rounded O, so dQ and dK
     stay within the roundings of ds (2^-9 rms each) and of the output."""
