@@ -323,10 +323,12 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
           for (int half = 0; half < 2; ++half) {
             fetch(half);
             tmem_wait_ld();
-            if (part) hide(half);
             if (kBias && exact) {
               score.template values<false>(v[0], nullptr);
               score.template values<false>(v[1], nullptr);
+            }
+            if (part) hide(half);        // after the cap, which would make a score of the mask
+            if (kBias && exact) {
 #pragma unroll
               for (int c = 0; c < 2; ++c)
 #pragma unroll

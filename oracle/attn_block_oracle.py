@@ -76,16 +76,16 @@ def visible(n, prefix, causal):
 
 
 def attention(Q, K, V, starts, heads, kv_heads, prefix=None, causal=True, scale=None, softcap=0.0, slopes=None,
-              dO=None, bounds=False):
+              dO=None, bounds=False, fp=2.0 ** -14):
     """Forward, and with dO the gradients: a dict of O, lse (dQ, dK, dV).
 
     bounds: also, under "tol", how far each output of a kernel may be off that
     rounds p and ds to bf16 for their products (half a step, 2^-8 relative,
     each), its outputs to bf16, and computes everything else in fp32 to a
-    relative 2^-14 of the terms it adds (fp32 products of up to 2^7 features
-    or sums of up to 2^9 keys lose at most 2^9 half steps of 2^-24 each, and
-    a score of magnitude up to 2^3 turns its own error into a relative error
-    of p eight times as large)."""
+    relative `fp` of the terms it adds: 2^-14 for scores of magnitude up to 2^3
+    (fp32 products of up to 2^7 features or sums of up to 2^9 keys lose at most
+    2^9 half steps of 2^-24 each, and a score of magnitude up to 2^3 turns its
+    own error into a relative error of p eight times as large)."""
     M = Q.shape[0]
     D = Q.shape[1] // heads
     scale = D ** -0.5 if scale is None else scale
@@ -96,7 +96,7 @@ def attention(Q, K, V, starts, heads, kv_heads, prefix=None, causal=True, scale=
         g = dO.reshape(M, heads, D)
         for name, like in (("dQ", q), ("dK", k), ("dV", v)):
             out[name], tol[name] = np.zeros_like(like), np.zeros_like(like)
-    half, fp = 2.0 ** -8, 2.0 ** -14
+    half = 2.0 ** -8
     for d in range(len(starts) - 1):
         a, e = int(starts[d]), int(starts[d + 1])
         n = e - a
