@@ -774,7 +774,11 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     AttnScore<kCap, kBias> score(p);
     const float2 mul = both(score.mul);
     uint32_t turn = 0, step = 0;
-    while (ok && items.advance()) {
+    // A wait that gives up is one warp's answer (another may have looked a moment
+    // later), and a warp that left for it would be missed at the barriers of
+    // whole_row, which have no limit.  So it carries ok = false to the next of
+    // them, whose answer all warps share: that one is the only way out.
+    while (items.advance()) {
       const AttnTileRef t = items.t;
       const int h = items.h;
       if (items.behind()) {
@@ -825,7 +829,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       float sum = 0.0f;
       if (n == 1) {
         // sum_j p_ij dp_ij
-        ok = mbar_wait_warp(&s_full[step & 1u], (step >> 1) & 1u, ctl) && mbar_wait_warp(dp_full, step & 1u, ctl);
+        ok = ok && mbar_wait_warp(&s_full[step & 1u], (step >> 1) & 1u, ctl) && mbar_wait_warp(dp_full, step & 1u, ctl);
         if (ok) {
           tc_fence_after();
           float2 two = make_float2(0.0f, 0.0f);
@@ -854,7 +858,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
           const int m = min(t.row0 + r0 + first + i, t.end - 1);
           o[i] = __ldg(reinterpret_cast<const uint4*>(p.O + (static_cast<size_t>(m) * p.heads + h) * D) + chunk);
         }
-        ok = mbar_wait_warp(qo_full, turn & 1u, ctl);
+        ok = ok && mbar_wait_warp(qo_full, turn & 1u, ctl);
         if (ok) {
 #pragma unroll
           for (int i = 0; i < kL; ++i) {
@@ -923,7 +927,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
       }
       if (kBias && n > 1) ok = whole_row(exact.x + exact.y, ok);
       ok = ok && mbar_wait_warp(acc_full, turn & 1u, ctl);
-      if (!ok) break;
+      if (!ok) continue;
       ++turn;
       tc_fence_after();
       // 64-byte pieces of a row: by all warps, or by the first half of them
