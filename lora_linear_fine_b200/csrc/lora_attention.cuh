@@ -279,11 +279,13 @@ __device__ __forceinline__ float2 attn_exp2(float2 x, int i) {
 // raw products (mul = scale log2(e)) or, with a cap, their tanh (mul = cap
 // log2(e)).
 //   tanh(y) = y P(y^2), P of degree 3 with the least largest error for
-//   |y| <= 0.4 (2^-23.3), where all of a warp's values are that small and the
-//   powers of scale / cap folded into P's coefficients are within fp32's range:
-//   FMAs alone, 5 for a pair.  Else tanh(y) = 1 - 2 / (1 + exp(2 y)), two
-//   special functions a value, right at both ends (0 and infinity in the
-//   denominator), within a few 2^-24.
+//   |y| <= 0.4 (2^-23.3), where the powers of scale / cap folded into P's
+//   coefficients are within fp32's range: FMAs alone, 5 for a pair.  Else
+//   tanh(y) = 1 - 2 / (1 + exp(2 y)), two special functions a value, right at
+//   both ends (0 and infinity in the denominator), within a few 2^-24.
+//   Each value goes by its own size, so it is the same bits whatever its
+//   neighbours in the tile are, which may be another document's; only the work
+//   for the second form depends on whether some value of the warp needs it.
 template <bool kCap, bool kBias>
 struct AttnScore {
   // Of four pairs of exponentials, those by the polynomial.  With a cap or a
@@ -318,16 +320,13 @@ struct AttnScore {
       }
       if (!__any_sync(0xffffffffu, fmaxf(top[0], top[1]) > limit)) {
 #pragma unroll
-        for (int e = 0; e < n; e += 2) {
-          const float2 s = pair_of(&v[e]), u = mul2(s, s);
-          float2 q = fma2(both(a3), u, both(a2));
-          q = fma2(q, u, both(a1));
-          q = fma2(q, u, both(a0));
-          put(v, e, mul2(s, q));
-        }
+        for (int e = 0; e < n; e += 2) put(v, e, near(pair_of(&v[e])));
       } else {
 #pragma unroll
-        for (int e = 0; e < n; ++e) v[e] = __float_as_uint(far(__uint_as_float(v[e])));
+        for (int e = 0; e < n; e += 2) {
+          const float2 s = pair_of(&v[e]), z = near(s);
+          put(v, e, make_float2(fabsf(s.x) <= limit ? z.x : far(s.x), fabsf(s.y) <= limit ? z.y : far(s.y)));
+        }
       }
       if constexpr (kWantDt) {
 #pragma unroll
@@ -343,6 +342,13 @@ struct AttnScore {
     if constexpr (!kCap) return s;
     const float u = s * s;
     return fabsf(s) <= limit ? s * fmaf(fmaf(fmaf(a3, u, a2), u, a1), u, a0) : far(s);
+  }
+  __device__ __forceinline__ float2 near(float2 s) const {
+    const float2 u = mul2(s, s);
+    float2 q = fma2(both(a3), u, both(a2));
+    q = fma2(q, u, both(a1));
+    q = fma2(q, u, both(a0));
+    return mul2(s, q);
   }
   __device__ __forceinline__ float far(float s) const {
     return fmaf(-2.0f, rcp_approx(1.0f + ex2(s * (2.0f * kLog2e * pre))), 1.0f);

@@ -286,6 +286,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
         continue;
       }
       const int row = t.row0 + x * T + (warp & 3) * 32 + lane;
+      const bool mine = row < t.end;         // rows past the document decide nothing
       int n_a;
       const int n = tiles_of(&n_a);
       const int nx = x == 0 ? n_a : (pair() ? n : 0);
@@ -353,14 +354,14 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
         };
         if (!fixed) {
           // a row without a finite score so far has neither a reference nor any sums
-          const bool fresh = __any_sync(0xffffffffu, m == -INFINITY);
+          const bool fresh = __any_sync(0xffffffffu, mine && m == -INFINITY);
           float mx = largest(fresh);
           if (fresh && m == -INFINITY) m = mx;
-          bool grow = mx > m + kAttnHeadroom;
+          bool grow = mine && mx > m + kAttnHeadroom;
           if (__any_sync(0xffffffffu, grow)) {
             if (kBias && !fresh) {
               mx = largest(true);
-              grow = mx > m + kAttnHeadroom;
+              grow = mine && mx > m + kAttnHeadroom;
             }
             if (j < nx - 1 && __any_sync(0xffffffffu, grow)) {
               ok = mbar_wait_warp(&pv_done[x], (step - 1) & 1u, ctl);
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
         }
         attn_store_rows<8>(w, out + f * 2, stride, t.end - row0, lane);
       }
-      if (row < t.end) {
+      if (mine) {
         // natural logarithm of sum exp z
         p.lse[static_cast<size_t>(row) * p.heads + h] = (m + log2f(total)) * 0.69314718056f;
       }

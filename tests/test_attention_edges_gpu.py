@@ -40,3 +40,30 @@ def test_steeply_rising_bias(D, cap, causal):
     change of base, the sum), which p turns into a relative 2^-11.9."""
     for k, lens in enumerate(([1], [5, 1, 127], [128, 2, 200])):
         _within_bounds(lens, 4, 2, D, fp=2.0 ** -11, cap=cap, slopes=[-1.0, -4.0, 0.5, -2.0], causal=causal, seed=30 + k)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("cap", [2.0, 30.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_documents_do_not_touch_each_other_under_a_cap(D, cap, bias):
+    """Large values, infinities and NaN in one document leave the other
+    documents' bits, whichever way they make the tanh be taken."""
+    import torch
+    lens = [100, 60, 200]
+
+    def poison(Q, K, V, dO):
+        Q[105], K[101], K[120], V[130] = (float("nan"), float("-inf"), float("inf"), float("nan"))
+        Q[112] = 1e20
+
+    def large(Q, K, V, dO):
+        Q[100:160] *= 64.0
+        K[100:160] *= 64.0
+
+    for causal in (True, False):
+        kw = dict(seed=16, causal=causal, cap=cap, slopes=[0.25, -0.02, 0.0, 0.01] if bias else None)
+        clean, _, _, _ = _run(lens, 40, 4, 2, D, **kw)
+        for edit in (poison, large):
+            out, _, _, _ = _run(lens, 40, 4, 2, D, edit=edit, **kw)
+            for name in clean:
+                assert torch.equal(out[name][:100], clean[name][:100]), name
+                assert torch.equal(out[name][160:], clean[name][160:]), name
