@@ -634,7 +634,7 @@ typedef struct lora_attn_desc {
     int32_t head_dim;    /* 64 or 128 (LORA_ERR_UNSUPPORTED otherwise) */
     int32_t causal;      /* 0: every row sees its whole document */
     float scale;         /* > 0, finite */
-    float softcap;       /* 0: none; else > 0, finite */
+    float softcap;       /* 0: none; else > 0, finite (above 2^60 scale it is taken for none) */
 } lora_attn_desc;
 
 /* The plan of a batch: its documents as lists of tiles.  It depends on the

@@ -144,6 +144,9 @@ __global__ void __launch_bounds__(1024)
 // ---------------------------------------------------------------------------
 // kernels
 // ---------------------------------------------------------------------------
+// How products become values (AttnScore).
+enum AttnTanh { kNoCap, kNearCap, kFarCap };
+
 struct AttnParams {
   AttnPlanView plan;
   const __nv_bfloat16 *Q, *K, *V, *dO;
@@ -156,6 +159,7 @@ struct AttnParams {
   int single;                    // forward: items of one tile
   int M, n_docs, heads, kv_heads;
   float scale, cap;              // cap 0: none
+  AttnTanh form;
 };
 
 __device__ __forceinline__ bool attn_plan_ok(const AttnParams& p) {
@@ -275,34 +279,55 @@ __device__ __forceinline__ float2 attn_exp2(float2 x, int i) {
   return (i & 3) < kPoly ? exp2_poly(x) : make_float2(ex2(x.x), ex2(x.y));
 }
 
-// A score's exponent of 2 is value * mul - slope2 |i - j|: the values are the
-// raw products (mul = scale log2(e)) or, with a cap, their tanh (mul = cap
-// log2(e)).
+// A score's exponent of 2 is value * mul - slope2 |i - j|.  Without a cap the
+// values are the raw products and mul = scale log2(e).  With one they are
+// top * tanh(y), y = scale / cap * product, and mul = cap log2(e) / top:
 //   tanh(y) = y P(y^2), P of degree 3 with the least largest error for
-//   |y| <= 0.4 (2^-23.3), where the powers of scale / cap folded into P's
-//   coefficients are within fp32's range: FMAs alone, 5 for a pair.  Else
+//   |y| <= 0.4 (2^-23.3): FMAs alone, 5 for a pair where the powers of
+//   scale / cap can be folded into P's coefficients.  Else
 //   tanh(y) = 1 - 2 / (1 + exp(2 y)), two special functions a value, right at
 //   both ends (0 and infinity in the denominator), within a few 2^-24.
 //   Each value goes by its own size, so it is the same bits whatever its
 //   neighbours in the tile are, which may be another document's; only the work
 //   for the second form depends on whether some value of the warp needs it.
-template <bool kCap, bool kBias>
+// kNearCap (scale / cap within (2^-17, 2^16)): top = 1, scale / cap is folded
+// into P.  kFarCap, for the others: y is formed first, since the folded
+// coefficients would leave fp32's range; with a cap far above the scores (as
+// good as none) top = cap / scale, so that values are near the products and
+// nothing is multiplied by the cap (an error of 2^-24 would be one of 2^-24 cap
+// in the score), with a cap far below the scale top = 1.  kFarCap is kernels of
+// its own: one for both, with its constants among the parameters, took the
+// forward 333 us for 291 where scores pass 0.4 of the cap (2 x 4096 tokens, 16 /
+// 4 heads of 128, cap 30).
+template <AttnTanh kTanh, bool kBias>
 struct AttnScore {
+  static constexpr bool kCap = kTanh != kNoCap, kFar = kTanh == kFarCap;
   // Of four pairs of exponentials, those by the polynomial.  With a cap or a
   // bias the FMA pipe is the busy one already.
   static constexpr int kPoly = kCap || kBias ? 0 : 1;
   float mul;
   float slope2 = 0.0f;
-  float pre = 0.0f, limit = 0.0f, a0 = 0.0f, a1 = 0.0f, a2 = 0.0f, a3 = 0.0f;
+  float limit = 0.0f, twice = 0.0f, a0 = 0.0f, a1 = 0.0f, a2 = 0.0f, a3 = 0.0f;
+  float turn = 1.0f, top = 1.0f, fall = -1.0f;
   __device__ __forceinline__ explicit AttnScore(const AttnParams& p) : mul((kCap ? p.cap : p.scale) * kLog2e) {
     if constexpr (kCap) {
-      pre = p.scale / p.cap;
-      limit = pre > 0x1p-17f && pre < 0x1p16f ? 0.4f / pre : -1.0f;
+      float pre = p.scale / p.cap;
+      if constexpr (kFar) {
+        turn = fminf(pre, 0x1.fffffep127f);
+        if (pre < 1.0f) {
+          top = p.cap / p.scale;
+          mul = p.scale * kLog2e;
+        }
+        fall = -1.0f / (top * top);
+        pre = 1.0f;
+      }
       const float u = pre * pre;
-      a0 = 0.9999998807907104f * pre;
-      a1 = -0.333313912153244f * pre * u;
-      a2 = 0.1327143758535385f * pre * u * u;
-      a3 = -0.04757281020283699f * pre * u * u * u;
+      limit = 0.4f / pre;
+      twice = 2.0f * kLog2e * pre;
+      a0 = 0.9999998807907104f * pre * top;
+      a1 = -0.333313912153244f * pre * u * top;
+      a2 = 0.1327143758535385f * pre * u * u * top;
+      a3 = -0.04757281020283699f * pre * u * u * u * top;
     }
   }
   __device__ __forceinline__ void head(const AttnParams& p, int h) {
@@ -312,13 +337,17 @@ struct AttnScore {
   template <bool kWantDt, int n>
   __device__ __forceinline__ void values(uint32_t (&v)[n], float2* dt) const {
     if constexpr (kCap) {
-      float top[2] = {0.0f, 0.0f};
+      if constexpr (kFar) {
+#pragma unroll
+        for (int e = 0; e < n; e += 2) put(v, e, mul2(pair_of(&v[e]), both(turn)));
+      }
+      float size[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int e = 0; e < n; e += 4) {
-        top[0] = max3_abs(top[0], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-        top[1] = max3_abs(top[1], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+        size[0] = max3_abs(size[0], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+        size[1] = max3_abs(size[1], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
       }
-      if (!__any_sync(0xffffffffu, fmaxf(top[0], top[1]) > limit)) {
+      if (!__any_sync(0xffffffffu, fmaxf(size[0], size[1]) > limit)) {
 #pragma unroll
         for (int e = 0; e < n; e += 2) put(v, e, near(pair_of(&v[e])));
       } else {
@@ -332,7 +361,7 @@ struct AttnScore {
 #pragma unroll
         for (int e = 0; e < n; e += 2) {
           const float2 t = pair_of(&v[e]);
-          dt[e / 2] = fma2(mul2(t, t), both(-1.0f), both(1.0f));
+          dt[e / 2] = fma2(mul2(t, t), both(fall), both(1.0f));
         }
       }
     }
@@ -340,8 +369,8 @@ struct AttnScore {
   // one product's value
   __device__ __forceinline__ float one(float s) const {
     if constexpr (!kCap) return s;
-    const float u = s * s;
-    return fabsf(s) <= limit ? s * fmaf(fmaf(fmaf(a3, u, a2), u, a1), u, a0) : far(s);
+    if constexpr (kFar) s *= turn;
+    return fabsf(s) <= limit ? near(both(s)).x : far(s);
   }
   __device__ __forceinline__ float2 near(float2 s) const {
     const float2 u = mul2(s, s);
@@ -351,7 +380,7 @@ struct AttnScore {
     return mul2(s, q);
   }
   __device__ __forceinline__ float far(float s) const {
-    return fmaf(-2.0f, rcp_approx(1.0f + ex2(s * (2.0f * kLog2e * pre))), 1.0f);
+    return fmaf(-2.0f * top, rcp_approx(1.0f + ex2(s * twice)), top);
   }
   // `base` minus the bias at distances d0 + c and d0 + c + 1 (either sign)
   __device__ __forceinline__ float2 shifted(float2 base, float d0, float c, float step) const {

@@ -78,10 +78,11 @@ struct AttnDkvCfg {
   static_assert(kSmemBytes <= kSmemLimitBytes, "shared memory");
 };
 
-template <int D, bool kCap, bool kBias>
+template <int D, AttnTanh kTanh, bool kBias>
 __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     attn_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnBwdMaps maps) {
   using C = AttnDkvCfg<D>;
+  constexpr bool kCap = kTanh != kNoCap;
   constexpr int T = kAttnTile, S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     auto part_of = [&](int part, int which) {
       return p.partial + static_cast<size_t>(2 * part + which) * p.M * p.kv_heads * D;
     };
-    AttnScore<kCap, kBias> score(p);
+    AttnScore<kTanh, kBias> score(p);
     const float2 mul = both(score.mul);
     RingPos r;
     uint32_t turn = 0, step = 0;
@@ -418,9 +419,9 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
           const float2 nl[2] = {make_float2(l.x, l.y), make_float2(l.z, l.w)};
 #pragma unroll
           for (int u = 0; u < 2; ++u)
-            AttnScore<kCap, kBias>::put(
+            AttnScore<kTanh, kBias>::put(
                 v[0], e + 2 * u,
-                attn_exp2<AttnScore<kCap, kBias>::kPoly>(fma2(pair_of(&v[0][e + 2 * u]), mul, score.shifted(nl[u], d0, e + 2 * u, 1.0f)),
+                attn_exp2<AttnScore<kTanh, kBias>::kPoly>(fma2(pair_of(&v[0][e + 2 * u]), mul, score.shifted(nl[u], d0, e + 2 * u, 1.0f)),
                                         e / 2 + u));
           if (e % (32 / kParts) == 32 / kParts - 4) {
             const int e0 = e + 4 - 32 / kParts;
@@ -563,10 +564,11 @@ struct AttnDqCfg {
   static_assert(kSmemBytes <= kSmemLimitBytes, "shared memory");
 };
 
-template <int D, bool kCap, bool kBias>
+template <int D, AttnTanh kTanh, bool kBias>
 __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     attn_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnBwdMaps maps) {
   using C = AttnDqCfg<D>;
+  constexpr bool kCap = kTanh != kNoCap;
   constexpr int T = kAttnTile, SK = C::kStagesK, SV = C::kStagesV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -771,7 +773,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
     const int quarter = (warp - 4) >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t rP = tP + lanes + 32 * quarter;
-    AttnScore<kCap, kBias> score(p);
+    AttnScore<kTanh, kBias> score(p);
     const float2 mul = both(score.mul);
     uint32_t turn = 0, step = 0;
     // A wait that gives up is one warp's answer (another may have looked a moment
@@ -802,7 +804,7 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
         const float d0 = static_cast<float>(j0 - row);
 #pragma unroll
         for (int e = 0; e < N; e += 2)
-          y[e / 2] = attn_exp2<AttnScore<kCap, kBias>::kPoly>(
+          y[e / 2] = attn_exp2<AttnScore<kTanh, kBias>::kPoly>(
               fma2(pair_of(&v[e]), mul, score.shifted(shift, d0, e, 1.0f)), e / 2);
         if (j0 + N > all) {
           const int lim = see - j0;

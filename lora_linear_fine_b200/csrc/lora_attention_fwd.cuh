@@ -51,11 +51,12 @@ struct AttnFwdMaps {
   CUtensorMap q, k, v;     // [M x heads * D] bf16, box 64 x 128, 128-byte swizzle
 };
 
-template <int D, bool kCap, bool kBias>
+template <int D, AttnTanh kTanh, bool kBias>
 __global__ void __launch_bounds__(kAttnFwdThreads, 1)
     attn_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnFwdMaps maps) {
   using C = AttnFwdCfg<D>;
-  constexpr int T = kAttnTile, S = C::kStages, kPoly = AttnScore<kCap, kBias>::kPoly;
+  constexpr bool kCap = kTanh != kNoCap;
+  constexpr int T = kAttnTile, S = C::kStages, kPoly = AttnScore<kTanh, kBias>::kPoly;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem + 2 * C::kTileBytes;
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
     const int x = (warp - 4) >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tbase + x * T + lanes, tO = tbase + 256 + x * T + lanes;
-    AttnScore<kCap, kBias> score(p);
+    AttnScore<kTanh, kBias> score(p);
     const float2 mul = both(score.mul);
     uint32_t step = 0;                       // key tiles of this warpgroup so far
     while (ok && items.advance()) {
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
       score.head(p, h);
       // rows of few keys take their maximum: p of the only key, or of one that
       // outweighs the others, is then 1 and needs no rounding
-      const bool fixed = kCap && nx > 1 && score.mul <= kAttnFixedRange && score.slope2 >= 0.0f;
+      const bool fixed = kCap && nx > 1 && p.cap * kLog2e <= kAttnFixedRange && score.slope2 >= 0.0f;
       float m = fixed ? 0.0f : -INFINITY;      // the reference, an exponent of 2
       float2 l = make_float2(0.0f, 0.0f);      // two partial sums
       for (int j = nx - 1; j >= 0 && ok; --j, ++step) {

@@ -10,6 +10,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <limits>
 #include <atomic>
 #include <vector>
 #include <map>
@@ -2297,7 +2298,13 @@ AttnParams attn_params(const lora_attn_desc* d, void* plan, const void* Q, const
   p.heads = d->heads;
   p.kv_heads = d->kv_heads;
   p.scale = d->scale;
-  p.cap = d->softcap;
+  // A cap above 2^60 scale changes scores of products below 2^47 by less than
+  // 2^-26 of themselves: it is none.
+  if (d->softcap > 0.0f && d->softcap <= 0x1p60 * d->scale) {
+    p.cap = d->softcap;
+    const float pre = p.scale / p.cap;
+    p.form = pre > 0x1p-17f && pre < 0x1p16f ? kNearCap : kFarCap;
+  }
   return p;
 }
 
@@ -2322,13 +2329,13 @@ bool attn_tm(CUtensorMap* tm, const void* ptr, const AttnParams& p, int heads, i
   return make_tm(tm, ptr, cols, static_cast<uint64_t>(p.M), cols, 64, kAttnTile);
 }
 
-template <int D, bool kCap, bool kBias>
+template <int D, AttnTanh kTanh, bool kBias>
 lora_status_t launch_attn_fwd(const AttnParams& p, int sms, cudaStream_t st) {
   AttnFwdMaps maps;
   if (!attn_tm(&maps.q, p.Q, p, p.heads, D) || !attn_tm(&maps.k, p.K, p, p.kv_heads, D) ||
       !attn_tm(&maps.v, p.V, p, p.kv_heads, D))
     return LORA_ERR_CUDA;
-  constexpr auto k = attn_fwd_kernel<D, kCap, kBias>;
+  constexpr auto k = attn_fwd_kernel<D, kTanh, kBias>;
   LORA_TRY(kernel_ready<k>(AttnFwdCfg<D>::kSmemBytes));
   const int64_t ctas = static_cast<int64_t>(p.single ? p.plan.max_q : p.plan.max_fwd) * p.heads;
   if (ctas > (int64_t(1) << 31) - 1) return LORA_ERR_UNSUPPORTED;
@@ -2336,21 +2343,28 @@ lora_status_t launch_attn_fwd(const AttnParams& p, int sms, cudaStream_t st) {
   return check_launch("attn_fwd_kernel");
 }
 
-template <int D>
-lora_status_t launch_attn_fwd_mod(const AttnParams& p, int sms, cudaStream_t st) {
-  if (p.cap > 0.0f)
-    return p.slopes != nullptr ? launch_attn_fwd<D, true, true>(p, sms, st) : launch_attn_fwd<D, true, false>(p, sms, st);
-  return p.slopes != nullptr ? launch_attn_fwd<D, false, true>(p, sms, st) : launch_attn_fwd<D, false, false>(p, sms, st);
+template <int D, AttnTanh kTanh>
+lora_status_t launch_attn_fwd_bias(const AttnParams& p, int sms, cudaStream_t st) {
+  return p.slopes != nullptr ? launch_attn_fwd<D, kTanh, true>(p, sms, st) : launch_attn_fwd<D, kTanh, false>(p, sms, st);
 }
 
-template <int D, bool kCap, bool kBias>
+template <int D>
+lora_status_t launch_attn_fwd_mod(const AttnParams& p, int sms, cudaStream_t st) {
+  switch (p.form) {
+    case kNearCap: return launch_attn_fwd_bias<D, kNearCap>(p, sms, st);
+    case kFarCap: return launch_attn_fwd_bias<D, kFarCap>(p, sms, st);
+    default: return launch_attn_fwd_bias<D, kNoCap>(p, sms, st);
+  }
+}
+
+template <int D, AttnTanh kTanh, bool kBias>
 lora_status_t launch_attn_bwd(const AttnParams& p, int sms, cudaStream_t st) {
   AttnBwdMaps maps;
   if (!attn_tm(&maps.q, p.Q, p, p.heads, D) || !attn_tm(&maps.k, p.K, p, p.kv_heads, D) ||
       !attn_tm(&maps.v, p.V, p, p.kv_heads, D) || !attn_tm(&maps.d_o, p.dO, p, p.heads, D))
     return LORA_ERR_CUDA;
-  constexpr auto kv = attn_dkv_kernel<D, kCap, kBias>;
-  constexpr auto q = attn_dq_kernel<D, kCap, kBias>;
+  constexpr auto kv = attn_dkv_kernel<D, kTanh, kBias>;
+  constexpr auto q = attn_dq_kernel<D, kTanh, kBias>;
   constexpr int kRegs = 128 * (kAttnBwdRegsLow + 4 * kAttnBwdRegsHigh);
   LORA_TRY(kernel_ready<kv>(AttnDkvCfg<D>::kSmemBytes, kAttnBwdThreads, kRegs));
   LORA_TRY(kernel_ready<q>(AttnDqCfg<D>::kSmemBytes, kAttnBwdThreads, kRegs));
@@ -2371,11 +2385,18 @@ lora_status_t launch_attn_bwd(const AttnParams& p, int sms, cudaStream_t st) {
   return LORA_OK;
 }
 
+template <int D, AttnTanh kTanh>
+lora_status_t launch_attn_bwd_bias(const AttnParams& p, int sms, cudaStream_t st) {
+  return p.slopes != nullptr ? launch_attn_bwd<D, kTanh, true>(p, sms, st) : launch_attn_bwd<D, kTanh, false>(p, sms, st);
+}
+
 template <int D>
 lora_status_t launch_attn_bwd_mod(const AttnParams& p, int sms, cudaStream_t st) {
-  if (p.cap > 0.0f)
-    return p.slopes != nullptr ? launch_attn_bwd<D, true, true>(p, sms, st) : launch_attn_bwd<D, true, false>(p, sms, st);
-  return p.slopes != nullptr ? launch_attn_bwd<D, false, true>(p, sms, st) : launch_attn_bwd<D, false, false>(p, sms, st);
+  switch (p.form) {
+    case kNearCap: return launch_attn_bwd_bias<D, kNearCap>(p, sms, st);
+    case kFarCap: return launch_attn_bwd_bias<D, kFarCap>(p, sms, st);
+    default: return launch_attn_bwd_bias<D, kNoCap>(p, sms, st);
+  }
 }
 
 }  // namespace

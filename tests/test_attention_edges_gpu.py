@@ -67,3 +67,67 @@ def test_documents_do_not_touch_each_other_under_a_cap(D, cap, bias):
             for name in clean:
                 assert torch.equal(out[name][:100], clean[name][:100]), name
                 assert torch.equal(out[name][160:], clean[name][160:]), name
+
+
+@pytest.mark.parametrize("cap", [1e4, 1e5, 1e6, 1e9, 1e25, 3e38])
+@pytest.mark.parametrize("D", [64, 128])
+def test_caps_far_above_the_scores(D, cap):
+    _within_bounds([200, 77, 260], 4, 2, D, cap=cap, seed=31)
+    _within_bounds([200, 77, 260], 4, 2, D, cap=cap, seed=32, slopes=[0.5, -0.01, 0.0, 1.0])
+
+
+@pytest.mark.parametrize("cap", [1e-3, 1.0, 55.0, 1e4, 1e7])
+@pytest.mark.parametrize("down", [-20, 3, 16, 18, 30, 50])
+@pytest.mark.parametrize("D", [64, 128])
+def test_capped_score_of_one_key(D, down, cap):
+    """lse of a row with one key is its score cap tanh(y), for |y| from about
+    2^-20 to 2^4 and scale / cap = 2^-down: to half steps of the sum of the
+    products and some sixteen of the result (near y = 0.4, where the tanh by the
+    exponential takes over, 2^-22 of it is twelve)."""
+    import lora_linear_fine_b200 as L
+    import torch
+    n = 48
+    Q, K, V, dO = (t.cuda() for t in _inputs(n, 2, 2, D, 33))
+    Q *= (2.0 ** (torch.linspace(-20, 4, n).floor() + down - 3)).bfloat16().cuda()[:, None]
+    plan = L.AttentionPlan(torch.arange(n + 1, dtype=torch.int32, device="cuda"), n)
+    c = float(np.float32(cap))
+    kw = dict(scale=c * 2.0 ** -down, softcap=c)
+    o, lse = L.attention(Q, K, V, plan, 2, 2, **kw)
+    dQ, dK, dV = L.attention_backward(dO, Q, K, V, o, lse, plan, 2, 2, **kw)
+    terms = kw["scale"] * G.host_f64(Q).reshape(n, 2, D) * G.host_f64(K).reshape(n, 2, D)
+    z = c * np.tanh(terms.sum(-1) / c)
+    off = np.abs(G.host_f64(lse) - z)
+    assert (off <= 2.0 ** -24 * (D * np.abs(terms).sum(-1) + 16 * np.abs(z))).all(), (off / np.abs(z)).max()
+    assert not dQ.any() and not dK.any()
+    # p and its sum are 2^e, e what the reference is off by: p is rounded to bf16 and then the quotient
+    near = lambda got, want, rows: (np.abs(G.host_f64(got[rows]) - G.host_f64(want[rows])) <=
+                                    2.0 ** -7 * (1 + 2.0 ** -8) * np.abs(G.host_f64(want[rows]))).all()
+    assert near(o, V, slice(None))
+    # the backward's p is exp(z - lse): within 2^-15 of 1 where z is below 2^6
+    assert near(dV, dO, np.abs(z).max(1) < 64)
+
+
+@pytest.mark.parametrize("down", [3, 18, 30])
+@pytest.mark.parametrize("cap", [1.0, 32.0])
+def test_gradients_of_capped_scores(cap, down):
+    """Documents of two equal keys, whose p is 1/2 whatever their score: dK
+    carries the cap's derivative, for scores of 2^-6 to twice the cap and
+    scale / cap = 2^-down."""
+    import lora_linear_fine_b200 as L
+    import torch
+    D, n = 64, 40
+    Q, K, V, dO = (t.cuda() for t in _inputs(2 * n, 2, 1, D, 34))
+    K[1::2] = K[::2]
+    Q *= (2.0 ** (torch.linspace(-6, 1, n).floor() + down - 3)).bfloat16().cuda().repeat_interleave(2)[:, None]
+    starts = np.arange(0, 2 * n + 1, 2)
+    plan = L.AttentionPlan(torch.from_numpy(starts).int().cuda(), 2 * n, causal=False)
+    kw = dict(scale=cap * 2.0 ** -down, softcap=cap)
+    o, lse = L.attention(Q, K, V, plan, 2, 1, **kw)
+    got = dict(zip(("dQ", "dK", "dV"), L.attention_backward(dO, Q, K, V, o, lse, plan, 2, 1, **kw)), O=o, lse=lse)
+    # scores up to 2^5: 2^-12 in place of the 2^-14 for scores up to 2^3
+    ref = O.attention(*(G.host_f64(t) for t in (Q, K, V)), starts, 2, 1, causal=False, dO=G.host_f64(dO), bounds=True,
+                      fp=2.0 ** -12, **kw)
+    for name, t in got.items():
+        t = G.host_f64(t)
+        assert np.isfinite(t).all(), name
+        assert (np.abs(t - ref[name]) <= ref["tol"][name] + 1e-30).all(), name
