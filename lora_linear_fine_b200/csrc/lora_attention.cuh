@@ -255,8 +255,8 @@ __device__ __forceinline__ float2 pair_of(const uint32_t* v) {
 // 2^x of a pair on the FMA pipe: x = n + f with n whole and |f| <= 1/2 (adding
 // 1.5 * 2^23 leaves n in the low bits), 2^f by a polynomial of degree 5 that is
 // 1 at 0 with the least largest relative error on that interval (2^-22.5 in
-// fp32), n added to the exponent.  From -127 down the result is 0 (1 with 127
-// taken off its exponent).  The special function unit gives 16 exponentials a
+// fp32), times 2^n.  From -127 down the result is 0 (the factor's exponent field
+// is).  NaN stays NaN, which n added to the bits of p would not leave.  The special function unit gives 16 exponentials a
 // cycle and SM, fewer than a tile's products leave time for; so the kernels
 // form part of them this way.
 __device__ __forceinline__ float2 exp2_poly(float2 x) {
@@ -269,8 +269,8 @@ __device__ __forceinline__ float2 exp2_poly(float2 x) {
   p = fma2(p, f, both(0.24022242426872253f));
   p = fma2(p, f, both(0.6931470036506653f));
   p = fma2(p, f, both(1.0f));
-  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+  return mul2(p, make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + 0x3f800000u),
+                             __uint_as_float((__float_as_uint(t.y) << 23) + 0x3f800000u)));
 }
 
 // 2^x of the i-th pair of a row: kPoly of four pairs by the polynomial.

@@ -408,7 +408,6 @@ __global__ void __launch_bounds__(kAttnFwdThreads, 1)
           if (half == 0) fetch(1);
           attn_publish(&p_full[2 * x + half], lane);       // the tensor core begins with the first half of the keys
         }
-        if (none) sum[0] = sum[1] = make_float2(0.0f, 0.0f);
         l = add2(l, add2(sum[0], sum[1]));
       }
       if (!ok || nx == 0) continue;

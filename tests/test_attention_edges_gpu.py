@@ -131,3 +131,25 @@ def test_gradients_of_capped_scores(cap, down):
         t = G.host_f64(t)
         assert np.isfinite(t).all(), name
         assert (np.abs(t - ref[name]) <= ref["tol"][name] + 1e-30).all(), name
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(cap=30.0), dict(slopes=[0.25, 0.0])], ids=["plain", "cap", "bias"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_nan_in_a_key(D, kw):
+    """A key of NaN, at every column of a group of eight: NaN in O, lse and dQ
+    of the rows that see it (by whatever form their exponentials are taken), no
+    change to the others; NaN in dV of every key that those rows see."""
+    import torch
+    for lens in ([16], [200]):
+        n = lens[0]
+        clean, _, _, _ = _run(lens, 0, 2, 1, D, seed=35, **kw)
+        for j in list(range(8)) + ([133] if n > 133 else []):
+            def edit(Q, K, V, dO):
+                K[j] = float("nan")
+
+            out, _, _, _ = _run(lens, 0, 2, 1, D, seed=35, edit=edit, **kw)
+            for name in ("O", "lse", "dQ"):
+                assert torch.isnan(out[name][j:]).all(), (name, j)
+            for name in ("O", "lse"):
+                assert torch.equal(out[name][:j], clean[name][:j]), (name, j)
+            assert torch.isnan(out["dV"]).all(), j
