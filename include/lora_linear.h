@@ -658,8 +658,8 @@ lora_status_t lora_linear_attn_plan(const int32_t* starts, const int32_t* prefix
 
 /* Forward.  Q, O [M x heads * head_dim] bf16, K, V [M x kv_heads * head_dim]
  * bf16, lse [M x heads] fp32 (written; natural logarithm); slopes: device fp32
- * [heads] or NULL.  plan: of this M, n_docs and causal; a plan of other sizes
- * sets its status bit 0x2 and nothing is computed.  A document whose rows hold
+ * [heads] or NULL.  plan: of this M, n_docs and causal; a plan of others sets
+ * its status bit 0x2 and nothing is computed.  A document whose rows hold
  * infinities or NaN leaves the other documents' results as they are; within the
  * document they may reach any row (a product with a p of zero).  A wait inside
  * the kernels that gives up sets the plan's status bit 0x1.  No workspace.  p

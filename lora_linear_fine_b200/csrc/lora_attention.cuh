@@ -35,6 +35,7 @@ enum : int {
   kPlanFwd = 18,         // tiles in each list
   kPlanQ = 19,
   kPlanKv = 20,
+  kPlanCausal = 21,
 };
 
 struct AttnPlanView {
@@ -110,6 +111,7 @@ __global__ void __launch_bounds__(1024)
     v.head[0] = good ? 0u : static_cast<uint32_t>(kStatusBadArgument);
     v.head[kPlanM] = static_cast<uint32_t>(M);
     v.head[kPlanDocs] = static_cast<uint32_t>(n_docs);
+    v.head[kPlanCausal] = static_cast<uint32_t>(causal);
     if (!good) v.head[kPlanFwd] = v.head[kPlanQ] = v.head[kPlanKv] = 0u;
   }
   if (!good) return;
@@ -157,13 +159,14 @@ struct AttnParams {
   float* partial;                // backward: [parts][2][M x kv_heads * D] sums of dk and dv (parts > 1)
   int parts, parts_log2;
   int single;                    // forward: items of one tile
-  int M, n_docs, heads, kv_heads;
+  int M, n_docs, causal, heads, kv_heads;
   float scale, cap;              // cap 0: none
   AttnTanh form;
 };
 
 __device__ __forceinline__ bool attn_plan_ok(const AttnParams& p) {
-  if (p.plan.head[kPlanM] == static_cast<uint32_t>(p.M) && p.plan.head[kPlanDocs] == static_cast<uint32_t>(p.n_docs))
+  if (p.plan.head[kPlanM] == static_cast<uint32_t>(p.M) && p.plan.head[kPlanDocs] == static_cast<uint32_t>(p.n_docs) &&
+      p.plan.head[kPlanCausal] == static_cast<uint32_t>(p.causal))
     return true;
   atomicOr(p.plan.head, static_cast<uint32_t>(kStatusBadArgument));
   return false;

@@ -2295,6 +2295,7 @@ AttnParams attn_params(const lora_attn_desc* d, void* plan, const void* Q, const
   p.lse = lse;
   p.M = static_cast<int>(d->M);
   p.n_docs = static_cast<int>(d->n_docs);
+  p.causal = d->causal;
   p.heads = d->heads;
   p.kv_heads = d->kv_heads;
   p.scale = d->scale;

@@ -153,3 +153,27 @@ def test_nan_in_a_key(D, kw):
             for name in ("O", "lse"):
                 assert torch.equal(out[name][:j], clean[name][:j]), (name, j)
             assert torch.isnan(out["dV"]).all(), j
+
+
+@pytest.mark.parametrize("made", [True, False])
+def test_plan_of_another_mask(made):
+    """A causal plan with a call for whole documents, or the reverse: status bit
+    0x2 and nothing computed, forward and backward."""
+    import lora_linear_fine_b200 as L
+    import torch
+    starts = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    Q, K, V, dO = (t.cuda() for t in _inputs(64, 2, 2, 64, 0))
+    st = torch.cuda.current_stream().cuda_stream
+    desc = L.make_attn_desc(64, 1, 2, 2, 64, causal=not made)
+    plan = L.AttentionPlan(starts, 64, causal=made)
+    o, lse = torch.full_like(Q, 3.0), torch.full((64, 2), 3.0, device="cuda")
+    assert L.lora_linear_attn_fwd(desc, plan.buf.data_ptr(), plan.nbytes, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+                                  None, o.data_ptr(), lse.data_ptr(), st) == 0
+    assert torch.all(o == 3.0) and torch.all(lse == 3.0) and plan.status() == 2
+    plan = L.AttentionPlan(starts, 64, causal=made)
+    ws = L.Workspace(L.lora_linear_attn_workspace_size(desc))
+    g = [torch.full_like(Q, 3.0) for _ in range(3)]
+    assert L.lora_linear_attn_bwd(desc, plan.buf.data_ptr(), plan.nbytes, dO.data_ptr(), Q.data_ptr(), K.data_ptr(),
+                                  V.data_ptr(), o.data_ptr(), lse.data_ptr(), None, *(t.data_ptr() for t in g),
+                                  ws.buf.data_ptr(), ws.nbytes, st) == 0
+    assert all(torch.all(t == 3.0) for t in g) and plan.status() == 2
