@@ -66,16 +66,19 @@ __device__ __forceinline__ void ln_unpack8(uint4 w, float2 (&f)[4]) {
 }
 
 // CTAs an SM: as many as the registers of a row in hand and the next one allow.
+// 1 / d comes as the sum of two fp32 numbers, so that the mean is rounded once: a
+// row of one value has exactly that mean, and x - mean is zero.  With 1 / d
+// rounded to one the mean could be a step off, which 1 / sqrt(eps) multiplies.
+// (16384 x 4096: 47.2 us, with a rounded 1 / d 46.8, with a division 47.8.)
 template <int T>
 __global__ void __launch_bounds__(LnCfg<T>::kThreads, LnCfg<T>::kPerSm)
     layernorm_fwd_kernel(const __nv_bfloat16* X, const __nv_bfloat16* __restrict__ g,
-                         const __nv_bfloat16* __restrict__ b, long long M, int d, float eps,
-                         __nv_bfloat16* Y, float* __restrict__ mean, float* __restrict__ rstd) {
+                         const __nv_bfloat16* __restrict__ b, long long M, int d, float inv_d, float inv_d_rest,
+                         float eps, __nv_bfloat16* Y, float* __restrict__ mean, float* __restrict__ rstd) {
   using C = LnCfg<T>;
   __shared__ float slots[2 * C::kGroups * C::kWarps * kLnSums];
   const int group = threadIdx.x / T, t = threadIdx.x % T;
   const int nv = d / 8;
-  const float inv_d = 1.0f / static_cast<float>(d);
   uint32_t phase = 0;
   grid_dep_wait();
   const long long step = static_cast<long long>(gridDim.x) * C::kGroups;
@@ -100,7 +103,7 @@ __global__ void __launch_bounds__(LnCfg<T>::kThreads, LnCfg<T>::kPerSm)
     fetch(row + step);
     float s[1] = {two.x + two.y};
     ln_group_sum<T, 1>(s, slots, group, phase);
-    const float mu = s[0] * inv_d;
+    const float mu = fmaf(s[0], inv_d, s[0] * inv_d_rest);
     two = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int v = 0; v < kLnNV; ++v)

@@ -2134,10 +2134,12 @@ lora_status_t check_layernorm(const void* X, const void* g, int64_t M, int64_t d
 template <int T>
 lora_status_t launch_ln_fwd(const void* X, const void* g, const void* b, int64_t M, int64_t d, float eps, void* Y,
                             float* mean, float* rstd, const DevInfo& dev, cudaStream_t st) {
+  const double inv_d = 1.0 / static_cast<double>(d);
+  const float inv = static_cast<float>(inv_d), rest = static_cast<float>(inv_d - inv);
   launch_k(layernorm_fwd_kernel<T>, dim3(ln_grid(M, T, LnCfg<T>::kPerSm, dev)), dim3(LnCfg<T>::kThreads), 0,
            st, false, static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(g),
-           static_cast<const __nv_bfloat16*>(b), static_cast<long long>(M), static_cast<int>(d), eps,
-           static_cast<__nv_bfloat16*>(Y), mean, rstd);
+           static_cast<const __nv_bfloat16*>(b), static_cast<long long>(M), static_cast<int>(d), inv,
+           rest, eps, static_cast<__nv_bfloat16*>(Y), mean, rstd);
   return check_launch("layernorm_fwd_kernel");
 }
 
