@@ -240,11 +240,13 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1)
     ++at;
     const uint8_t* xs = ln_smem + r.stage * stage_bytes;
     const uint8_t* ys = xs + sh.rows * x_bytes;
-    // kQ rows at a time, so that one round of sums serves them all
+    // kQ rows at a time, so that one round of sums serves them all.  x_hat is
+    // (x - mean) rstd, as in the forward: x rstd - mean rstd is an instruction
+    // less, but rounds mean rstd, which may be far larger than x_hat.
     for (int k = group; k < sh.rows; k += kQ * kGroups) {
-      float2 sc[kQ], sf[kQ];
+      float2 sc[kQ], nm[kQ];
 #pragma unroll
-      for (int q = 0; q < kQ; ++q) { sc[q] = both(rs[q]); sf[q] = both(-mu[q] * rs[q]); }
+      for (int q = 0; q < kQ; ++q) { sc[q] = both(rs[q]); nm[q] = both(-mu[q]); }
       if (k + kQ * kGroups < sh.rows) stats(row0, k + kQ * kGroups);
       else stats(row0 + gridDim.x * static_cast<long long>(sh.rows), group);
       if (k >= n) continue;
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1)
             ln_load8(gs + 8 * c, w);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              xh[e] = fma2(xh[e], sc[q], sf[q]);
+              xh[e] = mul2(add2(xh[e], nm[q]), sc[q]);
               ag[v][e] = fma2(dy[e], xh[e], ag[v][e]);
               ab[v][e] = add2(ab[v][e], dy[e]);
               const float2 dh = mul2(dy[e], w[e]);
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1)
             ln_load8(gs + 8 * c, w);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              xh[e] = fma2(xh[e], sc[q], sf[q]);
+              xh[e] = mul2(add2(xh[e], nm[q]), sc[q]);
               const float2 u = fma2(dy[e], mul2(w[e], sc[q]), fma2(xh[e], c2, c1));
               o[e] = pack_bf16x2(u.x, u.y);
             }
