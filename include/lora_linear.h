@@ -610,7 +610,8 @@ typedef struct lora_rotary_desc {
  * launch, by the table rows at each token's position (pos, cos, sin and n_pos of
  * `rope`; its head_dim is not read, its tables have rot / 2 columns).  The
  * features past rot are copied.  Yq may be Q and Yk may be K (both or neither:
- * LORA_ERR_INVALID_ARG).  A position outside the tables sets status bit 0x2 and
+ * LORA_ERR_INVALID_ARG); otherwise an output overlaps neither the other output
+ * nor an input (LORA_ERR_INVALID_ARG where they are the same).  A position outside the tables sets status bit 0x2 and
  * leaves that token unturned.  For q and k that come straight from a
  * LoRA projection in the half layout with whole heads of 64 or 128,
  * lora_linear_fwd_rope turns them before they are rounded.

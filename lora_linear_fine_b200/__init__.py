@@ -847,6 +847,9 @@ def rotary(Q, K, pos, cos, sin, head_dim, layout="half", inverse=False, inplace=
     bf16, f32, device = torch.bfloat16, torch.float32, Q.device
     _tensors(device, ("Q", Q, bf16, Q.shape), ("K", K, bf16, (M, k_cols)), ("pos", pos, torch.int32, (M,)),
              ("cos", cos, f32, cos.shape), ("sin", sin, f32, cos.shape))
+    if inplace and K is not None and M > 0 and (Q.data_ptr() < K.data_ptr() + 2 * K.numel() and
+                                                K.data_ptr() < Q.data_ptr() + 2 * Q.numel()):
+        _refuse("Q and K overlap: in place each would be turned twice")
 
     def run(st):
         Yq = Q if inplace else torch.empty_like(Q)

@@ -2492,7 +2492,8 @@ lora_status_t lora_linear_rotary(const lora_rotary_desc* d, const lora_rope_desc
       !aligned16(Yq) || !aligned16(Yk))
     return LORA_ERR_ALIGNMENT;
   const bool in_place = Yq == Q;
-  if (d->M > 0 && d->kv_heads > 0 && (Yk == K) != in_place) return LORA_ERR_INVALID_ARG;
+  if (d->M > 0 && d->kv_heads > 0 && ((Yk == K) != in_place || Yk == Yq || Yk == Q || Yq == K))
+    return LORA_ERR_INVALID_ARG;
   if (workspace == nullptr || workspace_bytes < kHeaderBytes || !aligned16(workspace)) return LORA_ERR_WORKSPACE;
   DevInfo dev;
   LORA_TRY(check_arch(&dev));
