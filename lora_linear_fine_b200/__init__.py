@@ -738,12 +738,16 @@ def _call(run, device, stream, *inputs):
         return run(st)
 
 
-def _workspace(workspace, nbytes, device):
+def _workspace(workspace, nbytes, device, stream):
+    """The workspace of a call, which `stream` (None: the current one) works in."""
     if workspace is None:
         return Workspace(nbytes, device)
     if workspace.buf.device != device:
         _refuse(f"the workspace is on {workspace.buf.device}, not {device}")
-    return workspace.ensure(nbytes)
+    workspace.ensure(nbytes)
+    if stream is not None:
+        workspace.buf.record_stream(stream)
+    return workspace
 
 
 def layer_norm(X, g, b=None, eps=1e-5, stream=None):
@@ -789,7 +793,7 @@ def layer_norm_backward(dY, X, g, mean, rstd, bias=True, workspace=None, stream=
         dX = torch.empty_like(X)
         dg = torch.empty(d, dtype=f32, device=device)
         db = torch.empty_like(dg) if bias else None
-        ws = _workspace(workspace, lora_linear_layernorm_workspace_size(M, d), device)
+        ws = _workspace(workspace, lora_linear_layernorm_workspace_size(M, d), device, stream)
         _check(_lib.lora_linear_layernorm_bwd(dY.data_ptr(), dY.dtype == f32, X.data_ptr(), g.data_ptr(),
                                               mean.data_ptr(), rstd.data_ptr(), M, d, dX.data_ptr(), dg.data_ptr(),
                                               _ptr(db), ws.buf.data_ptr(), ws.nbytes, st), "lora_linear_layernorm_bwd")
@@ -854,7 +858,7 @@ def rotary(Q, K, pos, cos, sin, head_dim, layout="half", inverse=False, inplace=
     def run(st):
         Yq = Q if inplace else torch.empty_like(Q)
         Yk = K if inplace or K is None else torch.empty_like(K)
-        ws = _workspace(workspace, 256, device)
+        ws = _workspace(workspace, 256, device, stream)
         desc = LoraRotaryDesc(M, q_cols // head_dim, k_cols // head_dim, head_dim, 2 * half, ROTARY_LAYOUTS[layout],
                               bool(inverse))
         rope = LoraRopeDesc(pos.data_ptr(), cos.data_ptr(), sin.data_ptr(), n_pos, head_dim)
@@ -945,7 +949,7 @@ def attention_backward(dO, Q, K, V, O, lse, plan, heads, kv_heads, scale=None, s
 
     def run(st):
         dQ, dK, dV = torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V)
-        ws = _workspace(workspace, _lib.lora_linear_attn_workspace_size(desc), device)
+        ws = _workspace(workspace, _lib.lora_linear_attn_workspace_size(desc), device, stream)
         _check(_lib.lora_linear_attn_bwd(desc, plan.buf.data_ptr(), plan.nbytes, dO.data_ptr(), Q.data_ptr(),
                                          K.data_ptr(), V.data_ptr(), O.data_ptr(), lse.data_ptr(), _ptr(slopes),
                                          dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.buf.data_ptr(), ws.nbytes, st),
