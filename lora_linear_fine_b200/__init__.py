@@ -894,7 +894,9 @@ class AttentionPlan:
         self.buf = _call(run, starts.device, stream, starts, prefix_len)
 
     def status(self, stream=None):
-        return lora_linear_device_status(self.buf.data_ptr(), _stream_handle(stream))[1]
+        import torch
+        with torch.cuda.device(self.buf.device):
+            return lora_linear_device_status(self.buf.data_ptr(), _stream_handle(stream))[1]
 
 
 def _attention_args(Q, K, V, plan, heads, kv_heads, scale, softcap, slopes):
