@@ -230,18 +230,28 @@ _lib = _LazyLib()
 
 
 class _LazyTorch:
-    """The torch functions' short way into the library (csrc/lora_torch.cpp), loaded on first use like it."""
+    """The torch functions' short way into the library (csrc/lora_torch.cpp),
+    loaded on first use like it.  It is bound to one interpreter and one torch;
+    where it is absent or does not load, every call declines (None), and the
+    functions below go the long way into the same library."""
 
     def __getattr__(self, name):
         import importlib.util
-        path = os.path.join(_PKG, "_lora_torch.so")
-        if not os.path.exists(path):
-            raise ImportError(f"{path} is missing: build it with `python -m lora_linear_fine_b200.build`")
+        import warnings
         import torch  # noqa: F401  (the module is linked with torch's libraries)
-        spec = importlib.util.spec_from_file_location("_lora_torch", path)
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
-        self.__dict__.update({k: v for k, v in vars(module).items() if not k.startswith("__")})
+        path = os.path.join(_PKG, "_lora_torch.so")
+        try:
+            spec = importlib.util.spec_from_file_location("_lora_torch", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+        except (ImportError, OSError) as e:
+            warnings.warn(f"{path} cannot be loaded ({e}): small calls take some 6 us more; build it with "
+                          "`python -m lora_linear_fine_b200.build`", RuntimeWarning, stacklevel=3)
+            decline = lambda *args: None
+            self.__dict__.update(dict.fromkeys(("layer_norm", "layer_norm_backward", "rotary_tables", "rotary", "attention",
+                                                "attention_backward"), decline))
+        else:
+            self.__dict__.update({k: v for k, v in vars(module).items() if not k.startswith("__")})
         return self.__dict__[name]
 
 
@@ -811,9 +821,10 @@ def rotary_tables(n_pos, rot, base=10000.0, scaling="none", factor=1.0, low=1.0,
         _refuse(f"scaling {scaling!r} is none of {sorted(ROTARY_SCALINGS)}")
     if n_pos < 0 or rot < 0:
         _refuse(f"n_pos {n_pos}, rot {rot}")
-    if device is None and stream is None and torch.cuda.is_initialized():
-        return _done(_torch.rotary_tables(n_pos, rot, base, ROTARY_SCALINGS[scaling], factor, low, high, original,
-                                          amplitude), "lora_linear_rotary_tables")
+    if device is None and stream is None and torch.cuda.is_initialized() and (
+            out := _torch.rotary_tables(n_pos, rot, base, ROTARY_SCALINGS[scaling], factor, low, high, original,
+                                        amplitude)) is not None:
+        return _done(out, "lora_linear_rotary_tables")
     if device is None:
         device = torch.device("cuda", torch.cuda.current_device()) if stream is None else stream.device
     device = torch.device(device)
