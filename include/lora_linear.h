@@ -665,7 +665,9 @@ lora_status_t lora_linear_attn_plan(const int32_t* starts, const int32_t* prefix
  * document they may reach any row (a product with a p of zero).  A wait inside
  * the kernels that gives up sets the plan's status bit 0x1.  No workspace.  p
  * is rounded to bf16 for the product with v; scores, sums and outputs are
- * accumulated in fp32. */
+ * accumulated in fp32.  Under a softcap up to 55 without negative slopes p is
+ * formed without a maximum, up to 2^80 before the division: with n keys a row,
+ * n |V| above 2^48 may overflow where all scores are at the cap. */
 lora_status_t lora_linear_attn_fwd(const lora_attn_desc* desc, void* plan, size_t plan_bytes, const void* Q,
                                    const void* K, const void* V, const float* slopes, void* O, float* lse,
                                    void* stream);
@@ -677,8 +679,10 @@ size_t lora_linear_attn_workspace_size(const lora_attn_desc* desc);
  * forward's O and lse.  The gradients of shared key / value heads are summed
  * over their query heads in fp32 in an order fixed by M, n_docs and the heads
  * (no atomics): the same bits in every call.  slopes get no gradient (frozen).
- * p and ds are rounded to bf16 for their products; sum_j p_ij dp_ij is formed in
- * fp32 for rows that see up to 128 keys, from the bf16 O otherwise.
+ * p and ds are rounded to bf16 for their products (with slopes, ds for dQ is the
+ * sum of two bf16 numbers).  sum_j p_ij dp_ij is formed in fp32 for rows of up to
+ * 128 keys, and for dK in all rows with slopes; from the bf16 O otherwise.  p
+ * comes from lse: scores of magnitude z put it off by a few 2^-24 z.
  * workspace >= lora_linear_attn_workspace_size(desc) bytes. */
 lora_status_t lora_linear_attn_bwd(const lora_attn_desc* desc, void* plan, size_t plan_bytes, const void* dO,
                                    const void* Q, const void* K, const void* V, const void* O, const float* lse,

@@ -36,6 +36,11 @@ the projections' epilogue does not cover, ``attention``):
     dq, dk, dv = attention_backward(dO, q, k, v, O, lse, plan, heads, kv_heads)
     dq, dk = rotary(dq, dk, pos, cos, sin, head_dim, inverse=True)
     dX, dg, db = layer_norm_backward(dXn, X, g, mean, rstd)
+
+Like ``forward`` and ``backward`` they record nothing for autograd: outputs do
+not require a gradient whatever the inputs do, and a training step calls the
+backward functions itself or from the ``backward`` of an autograd.Function of
+its own, as ``LoRALinearFunction`` does.
 """
 from __future__ import annotations
 
@@ -763,7 +768,8 @@ def _workspace(workspace, nbytes, device, stream):
 def layer_norm(X, g, b=None, eps=1e-5, stream=None):
     """(Y, mean, rstd): the layer norm of each row of X (bf16 [M x d]) with
     scale g and shift b (bf16 [d]; b may be None); mean, rstd fp32 [M] are the
-    backward's inputs."""
+    backward's inputs.  Not recorded for autograd: layer_norm_backward gives the
+    gradients."""
     import torch
     if stream is None and (out := _torch.layer_norm(X, g, b, eps)) is not None:
         return _done(out, "lora_linear_layernorm_fwd")
@@ -844,7 +850,10 @@ def rotary(Q, K, pos, cos, sin, head_dim, layout="half", inverse=False, inplace=
     """(Yq, Yk): the heads of Q [M x heads * head_dim] and K (bf16; K may be
     None) turned at the int32 positions pos [M] by the tables cos, sin
     [n_pos x rot/2]; the first rot features of each head take part.
-    ``inverse`` turns back: the gradients of Q and K from those of Yq and Yk."""
+    ``inverse`` turns back: the gradients of Q and K from those of Yq and Yk (not
+    recorded for autograd).  A position outside the tables leaves its token
+    unturned and sets bit 2 of the workspace's status(): pass a workspace to be
+    able to read it."""
     import torch
     if stream is None and workspace is not None and not inplace and layout in ROTARY_LAYOUTS and (
             out := _torch.rotary(Q, K, pos, cos, sin, head_dim, ROTARY_LAYOUTS[layout], inverse, workspace.buf)) is not None:
@@ -884,8 +893,11 @@ class AttentionPlan:
     ``attention_backward`` of every layer: starts (int32 [n_docs + 1], on the
     GPU) holds the documents' first rows and the end of the last one.  Without
     ``causal`` a row sees its whole document, with it the rows up to itself and
-    the first prefix_len (int32 [n_docs]) rows of its document.  status() is 2
-    if the offsets were not valid."""
+    the first prefix_len (int32 [n_docs]) rows of its document.  The offsets are
+    checked on the GPU: status() is 2 if they were not valid, and attention on
+    such a plan computes nothing, so that its outputs hold whatever their memory
+    held.  A batch whose offsets are not known to be good reads status() (which
+    waits for the stream) before it uses them."""
 
     def __init__(self, starts, M, prefix_len=None, causal=True, stream=None):
         import torch
@@ -929,7 +941,8 @@ def attention(Q, K, V, plan, heads, kv_heads, scale=None, softcap=0.0, slopes=No
     [M x kv_heads * head_dim]) within the plan's documents; scale None is
     1 / sqrt(head_dim), softcap caps the scores by a tanh, slopes (fp32
     [heads]) subtract slope * |i - j|.  lse fp32 [M x heads] is the backward's
-    input."""
+    input.  Not recorded for autograd: attention_backward gives the gradients.
+    With a plan whose status() is not 0 the outputs are not written."""
     import torch
     if stream is None and (out := _torch.attention(Q, K, V, plan.buf, plan.M, plan.n_docs, plan.causal, heads, kv_heads,
                                                    scale, softcap, slopes)) is not None:
@@ -949,7 +962,8 @@ def attention(Q, K, V, plan, heads, kv_heads, scale=None, softcap=0.0, slopes=No
 
 def attention_backward(dO, Q, K, V, O, lse, plan, heads, kv_heads, scale=None, softcap=0.0, slopes=None,
                        workspace=None, stream=None):
-    """(dQ, dK, dV) of ``attention`` for its O and lse."""
+    """(dQ, dK, dV) of ``attention`` for its O and lse; not written with a plan
+    whose status() is not 0."""
     import torch
     if stream is None and workspace is not None and (
             out := _torch.attention_backward(dO, Q, K, V, O, lse, plan.buf, plan.M, plan.n_docs, plan.causal, heads,

@@ -103,8 +103,6 @@ __global__ void __launch_bounds__(kAttnBwdThreads, 1)
   uint64_t* kv_full = st_empty + S;    // [NB]
   uint64_t* kv_empty = kv_full + NB;   // [NB]
   uint64_t* s_full = kv_empty + NB;    // [NS]
-  // [NS][kParts] parts of P from all warps.  One a buffer of S: with two, a
-  // warp may be at the next tile's P before another has finished this one's.
   // [NS][kParts]: a part of P from all warps.  One a buffer of S: with two of
   // them a warp may be at the next tile's P before another has finished this one's.
   uint64_t* p_full = s_full + NS;
