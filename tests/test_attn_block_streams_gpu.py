@@ -35,7 +35,7 @@ def test_a_workspace_outlives_the_work_on_another_stream():
         torch.cuda.synchronize()
         at = ws.buf.data_ptr()
         with torch.cuda.stream(side):
-            torch.cuda._sleep(20_000_000)           # some ten milliseconds
+            torch.cuda._sleep(100_000_000)          # some fifty milliseconds
         call(ws, side)
         del ws
         again = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
